@@ -19,7 +19,9 @@
 // Exactness.  The tensor cores cut an accumulator towards zero at every MMA; left in tensor
 // memory over 32768 tokens the output loses 1e-4 of itself.  So each step's product is
 // summed from zero and added to the row's fp32 registers, and the weights reach 2^15, where
-// their two fp16 parts keep 22 bits down to 2^-18 of the largest.
+// their two fp16 parts keep 22 bits down to 2^-18 of the largest.  A record with values past
+// fp16 (n s + z reaches 16 times the largest of its fields) holds them at a sixteenth, and its
+// products are added sixteen times.
 //
 // Few rows have few CTAs: their contexts are cut into parts, which leave their sums to the
 // CTAs of the second kernel.
@@ -69,6 +71,20 @@ __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
 }
 __device__ __forceinline__ void bar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void st_s8(uint32_t a, uint32_t v) {
+    asm volatile("st.shared.b8 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+// Whether a thread of two warps says so; a barrier of theirs (id)
+__device__ __forceinline__ bool pair_any(uint32_t id, bool yes) {
+    uint32_t r;
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred.aligned q, %2, 64, p;\n"
+        " selp.u32 %0, 1, 0, q;\n}\n"
+        : "=r"(r)
+        : "r"((uint32_t)yes), "r"(id)
+        : "memory");
+    return r != 0;
 }
 // one arrival per warp, after every lane's work
 __device__ __forceinline__ void warp_arrive(uint32_t bar, int lane) {
@@ -298,7 +314,8 @@ struct APlan {
     static constexpr uint32_t kNorm = kLut + 1024u;      // four steps of 64 floats
     static constexpr uint32_t kBars = kNorm + 4u * 4u * kStep;
     static constexpr uint32_t kMisc = kBars + 32u * 8u;  // tensor-memory base, abort flag, part, parts
-    static constexpr uint32_t kEnd = kMisc + 16u;
+    static constexpr uint32_t kSmall = kMisc + 16u;      // two stages: a byte per record, its values at a sixteenth
+    static constexpr uint32_t kEnd = kSmall + 16u;
     static_assert(kEnd <= 232448u, "227 KB per CTA");
 };
 // Barriers.  Step s is phase s / 2 of the ones kept per stage, s / 4 of NORM, s of the rest.
@@ -317,6 +334,7 @@ enum : uint32_t {
     B_QFULL = 24,  // the queries in place (one arrival per row warp)
     B_COUNT = 25
 };
+constexpr int kAgain = 16;  // products of a record whose values are held at a sixteenth
 constexpr uint32_t kTileCols = 256, kOCol = 128;  // tensor memory: two score buffers of 64, product
 
 // CUT: the contexts are cut into parts (what a part leaves behind takes registers that whole
@@ -359,6 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_rows_kernel(WArgs a) {
 
     const uint32_t sQ = base + PL::kQ, sK = base + PL::kK, sV = base + PL::kV;
     const uint32_t sLut = base + PL::kLut, sNorm = base + PL::kNorm, bars = base + PL::kBars;
+    const uint32_t sSmall = base + PL::kSmall;
     volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(psm + PL::kMisc);
     auto bar = [&](uint32_t id) { return bars + 8 * id; };
 
@@ -632,6 +651,34 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_rows_kernel(WArgs a) {
                 }
             }
         };
+        // Scale and zero point of the tokens of pair i that are there, else 0 (the fields of others
+        // may hold anything)
+        auto fields = [&](int s, int n, int i, float2& sf, float2& zf) {
+            const int t = kStep * s + 8 * (vg0 + 4 * n) + 2 * i;
+            const uint32_t m = there[n] ? (t < maxlim ? 0xffffu : 0u) | (t + 1 < maxlim ? 0xffff0000u : 0u) : 0u;
+            sf = __half22float2(u2h(vs[n][i] & m));
+            zf = __half22float2(u2h(vz[n][i] & m));
+        };
+        // Which of the warp's two records, as bits, hold values past fp16; with the other warp of
+        // those records (even and odd halves)
+        const uint32_t pair_bar = 1 + ((warp - 8) >> 1);
+        auto record_of = [&](int n) { return D == 128 ? n : lane >> 4; };
+        auto past_fp16 = [&](int s) {
+            bool past[2] = {false, false};
+#pragma unroll
+            for (int n = 0; n < NI; n++)
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    float2 sf, zf;
+                    fields(s, n, i, sf, zf);
+                    const float most = fmaxf(fmaxf(fabsf(zf.x), fabsf(fmaf(15.f, sf.x, zf.x))),
+                                             fmaxf(fabsf(zf.y), fabsf(fmaf(15.f, sf.y, zf.y))));
+                    past[0] |= record_of(n) == 0 && most > 65504.f;
+                    past[1] |= record_of(n) == 1 && most > 65504.f;
+                }
+            const uint32_t first = pair_any(pair_bar, past[0]);
+            return first | (uint32_t)pair_any(pair_bar, past[1]) << 1;
+        };
         if (nsteps > 0) {
             ids(0);
             load();
@@ -640,20 +687,38 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_rows_kernel(WArgs a) {
 #pragma unroll 1
         for (int s = 0; s < nsteps; s++) {
             const uint32_t st = (uint32_t)s & 1u;
+            // does a value pass fp16?  Not while every field is below 2^11 (0x6800): 15 s + |z| < 2^15
+            uint32_t top = 0;  // the largest fields, as bits of |.|
+#pragma unroll
+            for (int n = 0; n < NI; n++)
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    top = __vimax3_u16x2(top, vs[n][i] & 0x7fff7fffu, vz[n][i] & 0x7fff7fffu);
+            // the two warps of a record agree; one that gave up says so, and they leave together
+            uint32_t small = 0;
+            if (pair_any(pair_bar, ((top + 0x18001800u) & 0x80008000u) != 0 || !ok)) {
+                if (pair_any(pair_bar, !ok)) {
+                    ok = false;
+                    break;
+                }
+                small = past_fp16(s);
+            }
             if (s >= 2) ok = __all_sync(kFull, bar_wait(bar(B_VFREE + st), ((uint32_t)(s >> 1) + 1u) & 1u));
-            if (!ok) break;
+            if (!ok) continue;  // to the next agreement
+            if (vh == 0 && lane < 2) st_s8(sSmall + 4 * st + (uint32_t)((warp - 8) >> 1) + 2u * lane, small >> lane);
 #pragma unroll
             for (int n = 0; n < NI; n++) {
                 const uint32_t dst = sV + st * PL::kVStage + (uint32_t)(vq * 4096 + (vg0 + 4 * n) * 128 + vr * 16);
                 float2 sf[4], zf[4];
 #pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    // tokens that are not there are 0 (their fields may hold anything)
-                    const int t = kStep * s + 8 * (vg0 + 4 * n) + 2 * i;
-                    const uint32_t m =
-                        there[n] ? (t < maxlim ? 0xffffu : 0u) | (t + 1 < maxlim ? 0xffff0000u : 0u) : 0u;
-                    sf[i] = __half22float2(u2h(vs[n][i] & m));
-                    zf[i] = __half22float2(u2h(vz[n][i] & m));
+                for (int i = 0; i < 4; i++) fields(s, n, i, sf[i], zf[i]);
+                if (small) {
+                    const float f = (small >> record_of(n)) & 1u ? 1.f / kAgain : 1.f;
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        sf[i] = __fmul2_rn(sf[i], make_float2(f, f));
+                        zf[i] = __fmul2_rn(zf[i], make_float2(f, f));
+                    }
                 }
 #pragma unroll
                 for (int me = 0; me < 4; me++) {  // (mm, e): byte mm of the token's two, nibble e
@@ -821,6 +886,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_rows_kernel(WArgs a) {
                         for (int ks = 0; ks < kStep / 16; ks++)
                             mma_ts(el, tb + kOCol, pa + 16u * ks + (seg == 2 ? 8u : 0u),
                                    b + (seg == 1 ? PL::kVPart / 16 : 0u) + 16 * ks, idO, seg > 0 || ks > 0);
+                    // a record that holds a sixteenth, fifteen times more
+                    const uint32_t small = ld_s32(sSmall + 4 * st);
+                    if (__any_sync(kFull, small != 0)) {
+#pragma unroll 1
+                        for (int i = 0; i < 3 * (kAgain - 1) * (kStep / 16); i++) {
+                            const int seg = i % 3, ks = i / (3 * (kAgain - 1));
+                            if ((small >> (8 * ks)) & 1u)
+                                mma_ts(el, tb + kOCol, pa + 16u * ks + (seg == 2 ? 8u : 0u),
+                                       b + (seg == 1 ? PL::kVPart / 16 : 0u) + 16 * ks, idO, 1);
+                        }
+                    }
                     commit(el, bar(B_OFULL + t));
                 }
                 if (!ok) break;

@@ -1,0 +1,92 @@
+"""GPU tests of the eviction operators at the edges of their range: values and queries of
+extreme size, blocks that are not there, queries that are not numbers, long contexts."""
+import numpy as np
+import pytest
+import torch
+
+import workloads as W
+from evict_util import check_weights, weight_tolerance, weights_reference
+from parity_util import check_attention
+from workloads import bf16_bits
+
+pytestmark = pytest.mark.gpu
+
+
+def _status():
+    return torch.zeros(1, dtype=torch.int32, device="cuda")
+
+
+def _cuda(*a):
+    return [torch.from_numpy(np.ascontiguousarray(x)).cuda() for x in a]
+
+
+def _bf16(x):
+    return torch.from_numpy(np.asarray(x, np.float32)).to(torch.bfloat16)
+
+
+class Seq:
+    """One sequence of keys and values [L][Hkv][d] (bf16) in a cache of its own, and the
+    oracle's rows of the same tokens (float64)."""
+
+    def __init__(self, tq, orc, K, V, kind="tq", spare=0):
+        L, Hkv, d = K.shape
+        nblk = (L + 15) // 16
+        self.cache = tq.Cache(nblk + spare, Hkv, d, rotate=kind != "unrotated", bf16=kind == "bf16")
+        self.cache.data.fill_(0xFF)  # what lies behind the tokens reaches nothing
+        slots = np.arange(L, dtype=np.int32)
+        st = _status()
+        tq.quantize_append(K.cuda(), V.cuda(), *_cuda(slots), self.cache, status=st)
+        assert int(st.item()) == 0
+        self.bt = torch.arange(nblk, dtype=torch.int32, device="cuda").view(1, nblk)
+        self.lens = torch.tensor([L], dtype=torch.int32, device="cuda")
+        if kind == "bf16":
+            self.K, self.V = K.double().numpy()[None], V.double().numpy()[None]
+            return
+        rec = np.zeros((nblk, Hkv, orc.record_bytes(d)), np.uint8)
+        rot = kind != "unrotated"
+        orc.quantize_append(bf16_bits(K), bf16_bits(V), slots, rec, rotate=rot)
+        self.K, self.V = orc.dequantize(rec, Hkv, d, np.arange(nblk, dtype=np.int32)[None], np.array([L], np.int32), L,
+                                        rotate=rot)
+
+
+# ------------------------------------------------------------------ values of extreme size
+@pytest.mark.parametrize("d,L,n,window,spans", [
+    (128, 600, 40, 0, [(100, 101, 0.0, 7e4), (333, 340, -3e4, 9e4)]),  # few tokens of two steps
+    (128, 600, 40, 9, [(0, 600, 0.0, 7e4)]),                           # every token
+    (64, 700, 130, 5, [(695, 700, -6e4, 6e4)]),                        # only in the sight of the last rows
+    (64, 700, 130, 0, [(64, 128, 0.0, 9e5), (300, 301, -6.4e4, 9e5)]),
+    (128, 3000, 3, 0, [(1000, 1001, 0.0, 7e4), (2999, 3000, -3e4, 9e4)]),  # contexts cut into parts
+])
+def test_prefill_weights_value_ranges(tq, orc, d, L, n, window, spans):
+    """Groups whose scale and zero point fit fp16 while n s + z passes 65504, beside groups of
+    ordinary size: finite, and the rows that do not see such a token keep their accuracy.
+
+    Per dim the output is off by the weights' relative error times the mean of |v|; by the
+    fp16 parts of weights and values (2^-22 each, 2^-22 for the product of the low parts, and
+    2^-24 for n s + z); by a step's products, 12 or, where its four records are held at a
+    sixteenth, 192, cut by 2^-23 each, and the sum over L / 64 steps (2^-23 each); and by half a
+    step of the low part at a sixteenth, 2^-25 x 16."""
+    Hkv, G = 2, 4
+    rng = np.random.default_rng(L + d)
+    K = _bf16(rng.standard_normal((L, Hkv, d)))
+    V = rng.standard_normal((L, Hkv, d)).astype(np.float32)
+    for a, b, lo, hi in spans:
+        V[a:b] = rng.uniform(lo, hi, (b - a, Hkv, d))
+        V[a:b, :, :32] = rng.standard_normal((b - a, Hkv, 32))  # one group stays ordinary
+        V[a:b, :, 32], V[a:b, :, 33] = lo, hi                   # one spans the range
+    s = Seq(tq, orc, K, _bf16(V))
+    q = _bf16(rng.standard_normal((n, Hkv * G, d)))
+    qs = np.array([0, n], np.int32)
+    tw = torch.zeros((1, Hkv, L), device="cuda")
+    st = _status()
+    out = tq.prefill_attention_weights(q.cuda(), s.cache, s.bt, s.lens, *_cuda(qs), n, d ** -0.5, tw, window=window,
+                                       status=st).cpu().numpy()
+    assert int(st.item()) == 0 and np.isfinite(out).all()
+    qd = q.double().numpy()
+    want, add = weights_reference(qd, s.K, s.V, [L], d ** -0.5, qs, window)
+    tol = weight_tolerance(qd, s.K, [L], d ** -0.5, 0.0, (window or n) * G)
+    check_weights(tw.cpu().numpy(), add, tol(add))
+    mean_v = weights_reference(qd, s.K, np.abs(s.V), [L], d ** -0.5, qs, window)[0]
+    bound = (tol(np.float64(1.0)) + 3.25 * 2.0 ** -22 + (192 + L / 64) * 2.0 ** -23) * mean_v + 2.0 ** -21
+    err = np.abs(out - want)
+    assert np.all(err <= bound), float(np.max(err / bound))
