@@ -72,6 +72,13 @@ __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
 __device__ __forceinline__ void bar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+__device__ __forceinline__ uint2 ld_s64(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+    return v;
+}
+// bits 0 .. n - 1
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? ~0u : n > 0 ? (1u << n) - 1u : 0u; }
 __device__ __forceinline__ void st_s8(uint32_t a, uint32_t v) {
     asm volatile("st.shared.b8 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
@@ -175,6 +182,12 @@ __device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<__
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// NaN if one of them is
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
 // x - h, the part of x that its fp16 rounding h leaves (one mixed-precision fma)
@@ -315,7 +328,8 @@ struct APlan {
     static constexpr uint32_t kBars = kNorm + 4u * 4u * kStep;
     static constexpr uint32_t kMisc = kBars + 32u * 8u;  // tensor-memory base, abort flag, part, parts
     static constexpr uint32_t kSmall = kMisc + 16u;      // two stages: a byte per record, its values at a sixteenth
-    static constexpr uint32_t kEnd = kSmall + 16u;
+    static constexpr uint32_t kThere = kSmall + 16u;     // D = 64, four steps: bit t: token t is there
+    static constexpr uint32_t kEnd = kThere + 32u;
     static_assert(kEnd <= 232448u, "227 KB per CTA");
 };
 // Barriers.  Step s is phase s / 2 of the ones kept per stage, s / 4 of NORM, s of the rest.
@@ -334,6 +348,7 @@ enum : uint32_t {
     B_QFULL = 24,  // the queries in place (one arrival per row warp)
     B_COUNT = 25
 };
+constexpr uint32_t kAbsent = 0x7fc00001u;  // the norm of a token that is not there (a NaN that no fp16 gives)
 constexpr int kAgain = 16;  // products of a record whose values are held at a sixteenth
 constexpr uint32_t kTileCols = 256, kOCol = 128;  // tensor memory: two score buffers of 64, product
 
@@ -377,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_rows_kernel(WArgs a) {
 
     const uint32_t sQ = base + PL::kQ, sK = base + PL::kK, sV = base + PL::kV;
     const uint32_t sLut = base + PL::kLut, sNorm = base + PL::kNorm, bars = base + PL::kBars;
-    const uint32_t sSmall = base + PL::kSmall;
+    const uint32_t sSmall = base + PL::kSmall, sThere = base + PL::kThere;
     volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(psm + PL::kMisc);
     auto bar = [&](uint32_t id) { return bars + 8 * id; };
 
@@ -489,11 +504,25 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_rows_kernel(WArgs a) {
             tc_after_sync();
             const uint32_t tS = tT + (uint32_t)(s & 1) * kStep;
             const uint32_t nrm = sNorm + (uint32_t)(s & 3) * (4u * kStep);
-            // the row's maximum, then the weights; MASK: some row does not see the whole step
+            // the row's maximum, then the weights; MASK: some row does not see the whole step, or a
+            // token is not there.  Its norm makes the maximum NaN, with which the other variant
+            // ends, before it has written anything.
             float corr = 1.f;
             float2 l2 = make_float2(0.f, 0.f);
-            auto softmax = [&](auto mask) {
+            auto softmax = [&](auto mask) -> bool {
                 constexpr bool MASK = decltype(mask)::value;
+                // 16 tokens in flight at a time; at D = 64 there are registers for all 64,
+                // which then are read and scaled once
+                constexpr bool KEEP = D == 64;
+                // what the row sees: a bit a token, or where registers are short the limit and the
+                // norm of each (d 64: bits 300 us on 16 x 512 tokens at 4096, the other way 311;
+                // d 128: bits 2.74 ms on 2048 at 32768, the other way 2.60)
+                uint32_t see[2];
+                if constexpr (MASK && KEEP) {
+                    const uint2 there = ld_s64(sThere + 8u * (uint32_t)(s & 3));
+                    see[0] = there.x & low_bits(lim - kStep * s);
+                    see[1] = there.y & low_bits(lim - kStep * s - 32);
+                }
                 // scores 16 c + j .. + 3 times their norms, plus add
                 auto four = [&](const float* xc, int c, int j, float2 add, float2& y, float2& z) {
                     const uint4 nw = ld_s128(nrm + 64u * c + 4u * j);
@@ -501,17 +530,20 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_rows_kernel(WArgs a) {
                                    make_float2(__uint_as_float(nw.x), __uint_as_float(nw.y)), add);
                     z = __ffma2_rn(make_float2(xc[2], xc[3]),
                                    make_float2(__uint_as_float(nw.z), __uint_as_float(nw.w)), add);
-                    if (MASK) {
+                    if constexpr (MASK && KEEP) {
+                        const uint32_t b = see[c >> 1] >> (16 * (c & 1) + j);
+                        y.x = b & 1u ? y.x : -INFINITY;
+                        y.y = b & 2u ? y.y : -INFINITY;
+                        z.x = b & 4u ? z.x : -INFINITY;
+                        z.y = b & 8u ? z.y : -INFINITY;
+                    } else if constexpr (MASK) {
                         const int t = kStep * s + 16 * c + j;
-                        y.x = t < lim ? y.x : -INFINITY;
-                        y.y = t + 1 < lim ? y.y : -INFINITY;
-                        z.x = t + 2 < lim ? z.x : -INFINITY;
-                        z.y = t + 3 < lim ? z.y : -INFINITY;
+                        y.x = t < lim && nw.x != kAbsent ? y.x : -INFINITY;
+                        y.y = t + 1 < lim && nw.y != kAbsent ? y.y : -INFINITY;
+                        z.x = t + 2 < lim && nw.z != kAbsent ? z.x : -INFINITY;
+                        z.y = t + 3 < lim && nw.w != kAbsent ? z.y : -INFINITY;
                     }
                 };
-                // 16 tokens in flight at a time; at D = 64 there are registers for all 64,
-                // which then are read and scaled once
-                constexpr bool KEEP = D == 64;
                 constexpr int NX = KEEP ? 4 : 2;
                 float x[NX][16];
                 float m2[2] = {-INFINITY, -INFINITY};
@@ -530,11 +562,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_rows_kernel(WArgs a) {
                         float2 y, z;
                         four(xc + j, c, j, zero, y, z);
                         if (KEEP) xc[j] = y.x, xc[j + 1] = y.y, xc[j + 2] = z.x, xc[j + 3] = z.y;
-                        m2[0] = max3(m2[0], y.x, y.y);
-                        m2[1] = max3(m2[1], z.x, z.y);
+                        m2[0] = MASK ? max3(m2[0], y.x, y.y) : max3_nan(m2[0], y.x, y.y);
+                        m2[1] = MASK ? max3(m2[1], z.x, z.y) : max3_nan(m2[1], z.x, z.y);
                     }
                 }
-                const float mn = max3(m_run, m2[0], m2[1]);
+                const float mn = MASK ? max3(m_run, m2[0], m2[1]) : max3_nan(m_run, m2[0], m2[1]);
+                if (!MASK && __any_sync(kFull, isnan(mn))) return false;
                 corr = m_run == -INFINITY ? 1.f : exp2a(m_run - mn);
                 m_run = mn;
                 // a row that has seen no token yet takes 0 as its reference: 2^-inf = 0
@@ -568,11 +601,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_rows_kernel(WArgs a) {
                     }
                     tmem_st16u(tS + 16u * c, w);
                 }
+                return true;
             };
-            if (__all_sync(kFull, kStep * (s + 1) <= lim))
-                softmax(std::false_type{});
-            else
-                softmax(std::true_type{});
+            if (!__all_sync(kFull, kStep * (s + 1) <= lim) || !softmax(std::false_type{})) softmax(std::true_type{});
             asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             tc_before_sync();
             warp_arrive(bar(B_PFULL + 2 * tile + (s & 1)), lane);
@@ -801,9 +832,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_rows_kernel(WArgs a) {
                                            ld_s32(sLut + 4 * ((w >> 16) & 0xFFu)), ld_s32(sLut + 4 * (w >> 24))));
                     }
                 }
-                if (job0 < 64) {  // a token that is not there has norm 0 (its field may hold anything)
-                    const float norm = there0 && kStep * s + job0 < maxlim ? half_bits_to_float(kn) : 0.f;
-                    st_s32(sNorm + (uint32_t)(s & 3) * (4u * kStep) + 4u * job0, __float_as_uint(norm));
+                if (job0 < 64) {  // (behind the last token the field may hold anything)
+                    if constexpr (D == 64) {
+                        const uint32_t there = __ballot_sync(kFull, there0);
+                        if (lane == 0) st_s32(sThere + 8u * (uint32_t)(s & 3) + 4u * (uint32_t)(warp - 13), there);
+                    }
+                    const float norm = kStep * s + job0 < maxlim ? half_bits_to_float(kn) : 0.f;
+                    st_s32(sNorm + (uint32_t)(s & 3) * (4u * kStep) + 4u * job0,
+                           there0 ? __float_as_uint(norm) : kAbsent);
                 }
                 async_proxy_fence();
                 __syncwarp();

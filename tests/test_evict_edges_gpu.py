@@ -90,3 +90,57 @@ def test_prefill_weights_value_ranges(tq, orc, d, L, n, window, spans):
     bound = (tol(np.float64(1.0)) + 3.25 * 2.0 ** -22 + (192 + L / 64) * 2.0 ** -23) * mean_v + 2.0 ** -21
     err = np.abs(out - want)
     assert np.all(err <= bound), float(np.max(err / bound))
+
+
+# ------------------------------------------------------------------ blocks that are not there
+def _chunk_reference(q, K, V, L, scale, window, there):
+    """fp64 attention of a chunk over the tokens that are there (bool [L]); rows that see none
+    are 0 and have no vote.  q [n][Hq][d], K, V [L][Hkv][d]."""
+    n, Hq, _ = q.shape
+    Hkv = K.shape[1]
+    out, w = np.zeros(q.shape), np.zeros((Hkv, L))
+    seen = (np.arange(L)[None] <= (L - n + np.arange(n))[:, None]) & there[None]
+    some = seen.any(1)
+    for h in range(Hq):
+        kv = h // (Hq // Hkv)
+        x = np.where(seen, q[:, h] @ K[:, kv].T * scale, -np.inf)
+        p = np.where(seen, np.exp(x - np.where(some, x.max(1), 0)[:, None]), 0)
+        p /= np.where(some, p.sum(1), 1)[:, None]
+        out[:, h] = p @ V[:, kv]
+        w[kv] += p[max(0, n - (window or n)):].sum(0)
+    return out, w
+
+
+@pytest.mark.parametrize("d,Hkv,G,L,n,window,bad", [
+    (128, 2, 4, 400, 30, 0, [3, 24]),                       # one inside, one under the causal limits
+    (128, 2, 4, 400, 30, 7, [0, 1, 2, 3]),                  # a whole step
+    (64, 2, 8, 500, 100, 40, [30, 31]),                     # the last block among them
+    (128, 1, 4, 64, 64, 0, [0]),                            # the first rows see no token
+    (64, 1, 3, 200, 20, 0, list(range(13))),                # none is there
+    (128, 2, 4, 3000, 3, 0, [90] + list(range(100, 164))),  # contexts in parts, more than a part gone
+    (128, 8, 4, 3000, 3, 2, list(range(188))),
+])
+def test_prefill_weights_leave_absent_blocks_out(tq, orc, d, Hkv, G, L, n, window, bad):
+    """Tokens of a block id outside the cache are not there: they take no part in any row's
+    softmax, as in the decode."""
+    rng = np.random.default_rng(L + len(bad))
+    s = Seq(tq, orc, _bf16(rng.standard_normal((L, Hkv, d))), _bf16(rng.standard_normal((L, Hkv, d))))
+    bt = s.bt.clone()
+    bt[0, bad] = torch.tensor([-1 if i % 2 else s.cache.num_blocks for i in bad], dtype=torch.int32, device="cuda")
+    there = np.ones(L, bool)
+    for i in bad:
+        there[16 * i:16 * i + 16] = False
+    q = _bf16(rng.standard_normal((n, Hkv * G, d)))
+    before = rng.random((1, Hkv, L)).astype(np.float32)
+    tw = torch.from_numpy(before).cuda()
+    st = _status()
+    out = tq.prefill_attention_weights(q.cuda(), s.cache, bt, s.lens, *_cuda(np.array([0, n], np.int32)), n, d ** -0.5,
+                                       tw, window=window, status=st)
+    assert int(st.item()) == tq.STATUS_BAD_BLOCK
+    qd = q.double().numpy()
+    want, add = _chunk_reference(qd, s.K[0], s.V[0], L, d ** -0.5, window, there)
+    check_attention(out.cpu().numpy(), want)
+    got = tw.cpu().numpy()
+    assert np.array_equal(got[..., ~there], before[..., ~there])
+    tol = weight_tolerance(qd, s.K, [L], d ** -0.5, before.astype(np.float64), (window or n) * G)
+    check_weights(got, before.astype(np.float64) + add, tol(add))
