@@ -1027,7 +1027,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_split_kernel(DecodeArgs
                         for (int m = 0; m < KS; m++)
                             *reinterpret_cast<float2*>(dst + 16 * m) =
                                 pl[q] > 0.f ? make_float2(po[q][2 * m] / pl[q], po[q][2 * m + 1] / pl[q])
-                                            : make_float2(0.f, 0.f);
+                                // W: as the merge of a cut row leaves it, 0 without a token and NaN
+                                // where the scores are not numbers
+                                : W ? make_float2(po[q][2 * m] * 0.f, po[q][2 * m + 1] * 0.f)
+                                    : make_float2(0.f, 0.f);
                     } else {
                         const size_t pr = ((size_t)cu.r * 2 + (cu.i == cu.i_first ? 0 : 1)) * HPI + hq;
                         float* dst = a.ws_o + pr * D + 2 * g;

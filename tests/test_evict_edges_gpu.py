@@ -144,3 +144,26 @@ def test_prefill_weights_leave_absent_blocks_out(tq, orc, d, Hkv, G, L, n, windo
     assert np.array_equal(got[..., ~there], before[..., ~there])
     tol = weight_tolerance(qd, s.K, [L], d ** -0.5, before.astype(np.float64), (window or n) * G)
     check_weights(got, before.astype(np.float64) + add, tol(add))
+
+
+# ------------------------------------------------------------------ queries that are not numbers
+@pytest.mark.parametrize("num_splits", [0, 1, 3])
+@pytest.mark.parametrize("kind,d", [("tq", 128), ("tq", 64), ("unrotated", 128), ("bf16", 128), ("bf16", 64)])
+def test_a_decode_query_that_is_not_a_number(tq, orc, kind, d, num_splits):
+    """Its output is NaN however the context is cut, the other heads' rows are bit by bit those
+    without it, and the sums are those of the other heads."""
+    Hkv, G, L = 2, 5, 300
+    rng = np.random.default_rng(d)
+    s = Seq(tq, orc, _bf16(rng.standard_normal((L, Hkv, d))), _bf16(rng.standard_normal((L, Hkv, d))), kind)
+    q = _bf16(rng.standard_normal((1, Hkv * G, d))).cuda()
+    bad = q.clone()
+    bad[0, 1, 3] = float("nan")
+    bad[0, 7] = float("inf")
+    lost = torch.zeros(Hkv * G, dtype=torch.bool)
+    lost[1] = lost[7] = True
+    good, tw = (torch.zeros((1, Hkv, L), device="cuda") for _ in range(2))
+    want = tq.decode_attention_weights(q, s.cache, s.bt, s.lens, L, d ** -0.5, good, num_splits=num_splits)
+    out = tq.decode_attention_weights(bad, s.cache, s.bt, s.lens, L, d ** -0.5, tw, num_splits=num_splits)
+    assert torch.isnan(out[0, lost]).all() and torch.equal(out[0, ~lost], want[0, ~lost])
+    total = tw.sum(-1)[0].cpu()
+    assert torch.isfinite(tw).all() and torch.allclose(total, torch.tensor([G - 1.0, G - 1.0]), rtol=1e-5)
