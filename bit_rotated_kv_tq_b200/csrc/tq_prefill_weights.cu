@@ -1256,7 +1256,7 @@ cudaError_t launch_rows(const WArgs& a, cudaStream_t stream) {
     if (!regs_ok) return cudaErrorInvalidConfiguration;
     const dim3 grid((unsigned)(a.pairs * a.parts), (unsigned)a.Hkv, (unsigned)a.B);
     prefill_rows_kernel<D, CUT><<<grid, kThreads, APlan<D>::kEnd, stream>>>(a);
-    return cudaSuccess;
+    return cudaGetLastError();  // the votes add to the caller's sums: not without this kernel
 }
 
 template <int D>
