@@ -369,6 +369,8 @@ __global__ void __launch_bounds__(kBfWarps * 32) bf16_decode_kernel(DecodeArgs a
         l0 += __shfl_xor_sync(kFull, l0, m);
         l1 += __shfl_xor_sync(kFull, l1, m);
     }
+    // scores are missing: a sum that is not a number leaves the row without weights
+    if (W && aborted) l0 = l1 = NAN;
 
     // ---- merge the four warps (their rings are free now) in warp 0
     __syncthreads();

@@ -966,6 +966,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_split_kernel(DecodeArgs
                 pl[q] = lrun[q];
 #pragma unroll
                 for (int m = 4; m < 32; m <<= 1) pl[q] += __shfl_xor_sync(kFull, pl[q], m);
+                // scores are missing: a sum that is not a number leaves the row without weights
+                if (aborted) pl[q] = NAN;
             } else {
                 pl[q] = Z[q][2] + Z[q][3];
             }

@@ -636,8 +636,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_rows_kernel(WArgs a) {
         // ---- the row's output in dim order, or a part's sums, rows side by side, and what they
         // refer to
         const size_t at = (((size_t)b * a.Hkv + kv) * a.pairs + pair) * a.parts + part;
-        if (parts > 1)
-            a.part_stat[at * (2 * kRows) + tid] = ok ? make_float2(m_run, l_run) : make_float2(-INFINITY, 0.f);
+        if (parts > 1)  // (a part that gave up leaves its rows without a vote: their sums are not numbers)
+            a.part_stat[at * (2 * kRows) + tid] = make_float2(m_run, ok ? l_run : NAN);
         if (row_ok) {
             const float f = parts > 1 ? 1.f : ok && l_run > 0.f ? 1.f / l_run : 0.f;
             float4* dst = parts > 1 ? a.part_o + at * (2 * kRows * D / 4) + tid

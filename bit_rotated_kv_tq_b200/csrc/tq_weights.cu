@@ -76,20 +76,21 @@ __device__ __forceinline__ float2 row_stats(const DecodeArgs& a, const Parts& p,
         M = v.x;
         l = v.y;
     } else {
+        // (a part whose sum is not a number takes the row with it, even one without a maximum)
+        auto join = [&](float m2, float l2) {
+            const float Mn = fmaxf(M, m2);
+            const float f = M == -INFINITY ? 0.f : ex2(M - Mn), f2 = m2 == -INFINITY ? 0.f : ex2(m2 - Mn);
+            l = fmaf(f2, l2, f * l);
+            M = Mn;
+        };
         for (int r = p.first + lane; r <= p.last; r += 32) {
             const float2 v = a.ws_ml[p.slot(a, r)];
-            const float Mn = fmaxf(M, v.x);
-            if (Mn != -INFINITY) {
-                l = l * ex2(M - Mn) + v.y * ex2(v.x - Mn);
-                M = Mn;
-            }
+            join(v.x, v.y);
         }
 #pragma unroll
         for (int m = 16; m; m >>= 1) {
             const float Mo = __shfl_xor_sync(kFull, M, m), lo = __shfl_xor_sync(kFull, l, m);
-            const float Mn = fmaxf(M, Mo);
-            if (Mn != -INFINITY) l = l * ex2(M - Mn) + lo * ex2(Mo - Mn);
-            M = Mn;
+            join(Mo, lo);
         }
     }
     return l > 0.f ? make_float2(M, 1.f / l) : make_float2(0.f, 0.f);

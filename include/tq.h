@@ -78,7 +78,8 @@ enum {
     TQ_STATUS_RANGE = 4,     /* a key norm or value scale/zero overflowed fp16 */
     TQ_STATUS_BAD_LEN = 8,   /* seq_len < 0 or > max_blocks * 16 (treated as 0) */
     TQ_STATUS_TIMEOUT = 16,  /* a kernel gave up waiting (~1 s) for its own copy: the
-                                call's output is incomplete; never expected */
+                                call's output is incomplete, and rows it concerns add
+                                nothing to token_weights; never expected */
     TQ_STATUS_INTERNAL = 32  /* the decode kernel's shared-memory plan did not fit its
                                 allocation: nothing was computed; never expected */
 };

@@ -167,3 +167,41 @@ def test_a_decode_query_that_is_not_a_number(tq, orc, kind, d, num_splits):
     assert torch.isnan(out[0, lost]).all() and torch.equal(out[0, ~lost], want[0, ~lost])
     total = tw.sum(-1)[0].cpu()
     assert torch.isfinite(tw).all() and torch.allclose(total, torch.tensor([G - 1.0, G - 1.0]), rtol=1e-5)
+
+
+# ------------------------------------------------------------------ parts that are not numbers
+@pytest.mark.parametrize("call,kind,d", [("decode", "tq", 128), ("decode", "tq", 64), ("decode", "bf16", 128),
+                                         ("prefill", "tq", 128), ("prefill", "tq", 64)])
+def test_a_part_without_a_sum_leaves_its_rows_without_weights(tq, orc, call, kind, d):
+    """Records whose scores are not numbers, as many as one part of a cut context (what a part
+    that gave up waiting leaves looks the same): their head's rows are NaN and add nothing, as
+    where the context is whole, and the other head is as without them."""
+    Hkv, G, L, n = 2, 4, 3000, 3
+    rng = np.random.default_rng(d)
+    s = Seq(tq, orc, _bf16(rng.standard_normal((L, Hkv, d))), _bf16(rng.standard_normal((L, Hkv, d))), kind)
+    q = _bf16(rng.standard_normal((1 if call == "decode" else n, Hkv * G, d))).cuda()
+    before = torch.from_numpy(rng.random((1, Hkv, L)).astype(np.float32)).cuda()
+
+    def run(splits):
+        tw = before.clone()
+        if call == "decode":
+            out = tq.decode_attention_weights(q, s.cache, s.bt, s.lens, L, d ** -0.5, tw, num_splits=splits)
+        else:
+            out = tq.prefill_attention_weights(q, s.cache, s.bt, s.lens, *_cuda(np.array([0, n], np.int32)), n,
+                                               d ** -0.5, tw)
+        return out, tw
+
+    # ranges of at least one record (decode), parts of eight steps and more (prompt: from an
+    # eighth of the context on, far more than one part)
+    splits = 188 if call == "decode" else 0
+    want, sums = run(splits)
+    bad = slice(6, 7) if call == "decode" else slice(24, 120)
+    if kind == "bf16":
+        s.cache.data[bad, 0, :32 * d].view(torch.int16)[:] = 0x7fc0
+    else:
+        s.cache.data[bad, 0, 8 * d:8 * d + 32].view(torch.int16)[:] = 0x7e00
+    for k in (splits, 1):
+        out, tw = run(k)
+        assert torch.isnan(out[:, :G]).all() and torch.equal(tw[0, 0], before[0, 0])
+        if k == splits:
+            assert torch.equal(out[:, G:], want[:, G:]) and torch.equal(tw[0, 1], sums[0, 1])
