@@ -99,7 +99,10 @@ def _check(rc: int):
         raise TQError(rc, load().tq_last_error().decode())
 
 
-_current_device = torch._C._cuda_getDevice  # what torch.cuda.current_device() returns
+def _current_device():
+    """torch.cuda.current_device(), in one step where this torch has it."""
+    get = getattr(torch._C, "_cuda_getDevice", None)
+    return torch.cuda.current_device() if get is None else get()
 
 
 def _ptr(t):
@@ -110,7 +113,8 @@ def _stream(stream):
     """The cudaStream_t of a torch stream (None: the current one of the current device)."""
     if stream is not None:
         return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(_current_device())  # current_stream() costs 3 us more
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # current_stream() costs 3 us more
+    return torch.cuda.current_stream().cuda_stream if raw is None else raw(_current_device())
 
 
 def _dev(t, dtype, name):
