@@ -773,14 +773,18 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_split_kernel(DecodeArgs
             const float sc = a.rotate ? a.scale_log2 * rsqrtf((float)D) : a.scale_log2;
             const uint32_t dh = P.qh + (uint32_t)(((half * HPI + hw) * D + lane * EPL) * 2);
             const uint32_t dl = P.ql + (uint32_t)(((half * HPI + hw) * D + lane * EPL) * 2);
+            uint32_t top = 0;  // W: the largest element, bits of |.|
 #pragma unroll
             for (int e = 0; e < EPL; e += 2) {
                 const float y0 = x[e] * sc, y1 = x[e + 1] * sc;
                 const __half2 hp = __floats2half2_rn(y0, y1);
+                if constexpr (W) top = __vmaxu2(top, h2u(hp) & 0x7fff7fffu);
                 const float2 hf = __half22float2(hp);
                 sts32(dh + 2 * e, h2u(hp));
                 sts32(dl + 2 * e, h2u(__floats2half2_rn(y0 - hf.x, y1 - hf.y)));
             }
+            // infinite or not a number: no score of the row is one
+            if (W && ((top + 0x04000400u) & 0x80008000u)) flag_status(a.status, TQ_STATUS_RANGE);
         }
         half_sync(half);
 

@@ -252,7 +252,8 @@ struct QRows {
         for (int j = 0; j < NJ; j++)
             raw[j] = src ? ldg_u128(src + 8 * (4 * j + (lane >> 3))) : make_uint4(0, 0, 0, 0);
     }
-    __device__ __forceinline__ void rotate(const WArgs& a, uint32_t dst, int lane) const {
+    // false: an element is beyond fp16 or not a number, and so will be the row's scores
+    __device__ __forceinline__ bool rotate(const WArgs& a, uint32_t dst, int lane) const {
         float2 x[4 * NJ];
 #pragma unroll
         for (int j = 0; j < NJ; j++) {
@@ -287,6 +288,7 @@ struct QRows {
         // the +-1 butterfly leaves a factor sqrt(D) that the scale takes out
         const float sc = a.rotate ? a.scale_log2 * rsqrtf((float)D) : a.scale_log2;
         const float2 sc2 = make_float2(sc, sc);
+        uint32_t top = 0;  // the largest element, bits of |.|
 #pragma unroll
         for (int j = 0; j < NJ; j++) {
             uint32_t hi[4], lo[4];
@@ -297,8 +299,11 @@ struct QRows {
                 hi[e] = h2u(h);
                 lo[e] = pack_h2(rest_of(v.x, __low2half(h)), rest_of(v.y, __high2half(h)));
             }
+            top = __vimax3_u16x2(top, hi[0] & 0x7fff7fffu, hi[1] & 0x7fff7fffu);
+            top = __vimax3_u16x2(top, hi[2] & 0x7fff7fffu, hi[3] & 0x7fff7fffu);
             store(dst, j, lane, make_uint4(hi[0], hi[1], hi[2], hi[3]), make_uint4(lo[0], lo[1], lo[2], lo[3]));
         }
+        return ((top + 0x04000400u) & 0x80008000u) == 0;  // 0x7c00: infinite
     }
     __device__ __forceinline__ void zero(uint32_t dst, int lane) const {
 #pragma unroll
@@ -454,10 +459,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_rows_kernel(WArgs a) {
             for (int i = 0; i < n8; i++) {
                 load(next, i + 1);
                 const uint32_t dst = sQ + (uint32_t)(8 * i + warp) * (32u * D);
-                if (row0 + 64 * i + 8 * warp < rows_b)
-                    cur.rotate(a, dst, lane);
-                else
+                if (row0 + 64 * i + 8 * warp >= rows_b)
                     cur.zero(dst, lane);
+                else if (!cur.rotate(a, dst, lane))
+                    flag_status(a.status, TQ_STATUS_RANGE);
                 cur = next;
             }
             async_proxy_fence();

@@ -75,7 +75,8 @@ enum {
 enum {
     TQ_STATUS_BAD_SLOT = 1,  /* append: slot or logical slot outside the cache / table */
     TQ_STATUS_BAD_BLOCK = 2, /* a block-table entry outside [0, num_blocks) */
-    TQ_STATUS_RANGE = 4,     /* a key norm or value scale/zero overflowed fp16 */
+    TQ_STATUS_RANGE = 4,     /* append: a key norm or value scale/zero overflowed fp16;
+                                attention with token weights: a query too large (below) */
     TQ_STATUS_BAD_LEN = 8,   /* seq_len < 0 or > max_blocks * 16 (treated as 0) */
     TQ_STATUS_TIMEOUT = 16,  /* a kernel gave up waiting (~1 s) for its own copy: the
                                 call's output is incomplete, and rows it concerns add
@@ -269,7 +270,13 @@ TQ_API int tq_prefill_attention(const void* q, const tq_cache_t* cache, const ui
  * not depend on the order of the cached tokens (a rotary position is in the key already),
  * and the order of the kept tokens stays ascending, so decode, append and prefill go on
  * over the compacted cache with the new lengths.  These calls take at most 2^30 tokens a
- * sequence (max_blocks <= 2^26, else TQ_ERR_UNSUPPORTED). */
+ * sequence (max_blocks <= 2^26, else TQ_ERR_UNSUPPORTED).
+ *
+ * Queries: the attention over a TQ4/4 or unrotated cache holds scale log2(e) times the
+ * (rotated) query in two fp16 parts.  A row of which an element passes 65504, or is not a
+ * number, sets TQ_STATUS_RANGE; its output is NaN, and a row whose scores are not numbers
+ * adds nothing to the weights, over any cache.  (tq_decode_attention and
+ * tq_prefill_attention have the same limit, without the status.) */
 
 /* tq_decode_attention, which also adds each cached token's attention weight, summed over
  * the query heads of its kv head:

@@ -205,3 +205,45 @@ def test_a_part_without_a_sum_leaves_its_rows_without_weights(tq, orc, call, kin
         assert torch.isnan(out[:, :G]).all() and torch.equal(tw[0, 0], before[0, 0])
         if k == splits:
             assert torch.equal(out[:, G:], want[:, G:]) and torch.equal(tw[0, 1], sums[0, 1])
+
+
+# ------------------------------------------------------------------ queries of extreme size
+@pytest.mark.parametrize("kind", ["tq", "unrotated"])
+@pytest.mark.parametrize("call", ["decode", "prefill", "prefill in parts"])
+def test_queries_at_the_limit_of_fp16(tq, orc, kind, call):
+    """A query is held as fp16 parts of scale log2(e) times its rotated elements.  Up to 65504
+    they give the fp64 result (small keys bring the scores back to ordinary size); a row that
+    passes it sets TQ_STATUS_RANGE and has no weights, and the other rows are as without it."""
+    Hkv, G, d, L = 2, 4, 128, 1500 if call == "prefill in parts" else 300
+    n = 3 if call == "prefill in parts" else 1 if call == "decode" else 40
+    rng = np.random.default_rng(n)
+    small = 2.0 ** -14
+    s = Seq(tq, orc, _bf16(small * rng.standard_normal((L, Hkv, d))), _bf16(rng.standard_normal((L, Hkv, d))), kind)
+    qs = np.array([0, n], np.int32)
+    # rotated elements of normal numbers stay below 5.5 here; scaled by 2^15 / 5.5, below 2^15
+    scale = d ** -0.5
+    q = _bf16(rng.standard_normal((n, Hkv * G, d)) * (2.0 ** 15 / 5.5 / 1.4427 / scale * 0.99))
+
+    def run(q, status):
+        tw = torch.zeros((1, Hkv, L), device="cuda")
+        if call == "decode":
+            return tq.decode_attention_weights(q.cuda(), s.cache, s.bt, s.lens, L, scale, tw, status=status), tw
+        return tq.prefill_attention_weights(q.cuda(), s.cache, s.bt, s.lens, *_cuda(qs), n, scale, tw, status=status), tw
+
+    st = _status()
+    out, tw = run(q, st)
+    assert int(st.item()) == 0
+    qd = q.double().numpy()
+    want, add = weights_reference(qd, s.K, s.V, [L], scale, None if call == "decode" else qs)
+    check_attention(out.cpu().numpy(), want)
+    tol = weight_tolerance(qd, s.K, [L], scale, 0.0, n * G)
+    check_weights(tw.cpu().numpy(), add, tol(add))
+    big = q.clone()
+    big[0, 2] *= 64  # its largest element passes 2^16
+    out2, tw2 = run(big, st)
+    assert int(st.item()) == tq.STATUS_RANGE
+    keep = torch.ones((n, Hkv * G), dtype=torch.bool)
+    keep[0, 2] = False
+    assert torch.equal(out2.cpu()[keep], out.cpu()[keep]) and torch.isfinite(tw2).all()
+    # a row's weights sum to 1 as closely as each of them is good
+    assert torch.allclose(tw2.sum(-1)[0].cpu(), torch.tensor([n * G - 1.0, n * G]), rtol=float(tol(np.float64(1.0))))
