@@ -99,10 +99,10 @@ def _check(rc: int):
         raise TQError(rc, load().tq_last_error().decode())
 
 
-def _current_device():
-    """torch.cuda.current_device(), in one step where this torch has it."""
-    get = getattr(torch._C, "_cuda_getDevice", None)
-    return torch.cuda.current_device() if get is None else get()
+# torch's own shortcuts, where this torch has them (one without CUDA does not): a call passes here
+# several times
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # current_stream() costs 3 us more
 
 
 def _ptr(t):
@@ -113,8 +113,7 @@ def _stream(stream):
     """The cudaStream_t of a torch stream (None: the current one of the current device)."""
     if stream is not None:
         return stream.cuda_stream
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # current_stream() costs 3 us more
-    return torch.cuda.current_stream().cuda_stream if raw is None else raw(_current_device())
+    return torch.cuda.current_stream().cuda_stream if _raw_stream is None else _raw_stream(_current_device())
 
 
 def _dev(t, dtype, name):
