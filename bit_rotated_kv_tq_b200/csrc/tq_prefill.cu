@@ -95,12 +95,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(PrefillArgs a) {
     const int b = blockIdx.z, kv = blockIdx.y, tile = blockIdx.x;
     const int G = a.Hq / a.Hkv;
 
-    const int q0 = a.q_start[b];
-    int qlen = a.q_start[b + 1] - q0;
-    if (q0 < 0 || qlen < 0 || q0 + qlen > a.T) {  // rows outside q / out: nothing is touched
+    const int q0 = a.q_start[b], q1 = a.q_start[b + 1];
+    if (q0 < 0 || q1 < q0 || q1 > a.T) {  // rows outside q / out: nothing is touched
         if (tid == 0 && kv == 0 && tile == 0) flag_status(a.status, TQ_STATUS_BAD_LEN);
         return;
     }
+    const int qlen_full = q1 - q0;  // positions count from the chunk's full length
+    int qlen = qlen_full;
     if (qlen > a.max_q_len) {  // beyond the grid: the chunk is cut (its last rows are not written)
         if (tid == 0 && kv == 0 && tile == 0) flag_status(a.status, TQ_STATUS_BAD_LEN);
         qlen = a.max_q_len;
@@ -108,11 +109,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(PrefillArgs a) {
     const int rows_b = qlen * G;
     if (qlen <= 0 || tile * kRows >= rows_b) return;  // the whole CTA leaves together
     int L = a.seq_lens[b];
-    if (L < a.q_start[b + 1] - q0 || L > a.max_blocks * kBlock) {  // no valid context: rows get 0
+    if (L < qlen_full || L > a.max_blocks * kBlock) {  // no valid context: rows get 0
         if (tid == 0 && kv == 0 && tile == 0) flag_status(a.status, TQ_STATUS_BAD_LEN);
         L = -1;
     }
-    const int qlen_full = a.q_start[b + 1] - q0;  // positions count from the chunk's full length
     // this thread's row: chunk token i, query head kv * G + hh; it sees positions < lim
     const int R_ = tile * kRows + tid;
     const bool row_ok = R_ < rows_b;  // a row of the chunk (its output is written)

@@ -371,13 +371,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_rows_kernel(WArgs a) {
     const int pair = CUT ? blockIdx.x % a.pairs : blockIdx.x, part0 = CUT ? blockIdx.x / a.pairs : 0;
     const int G = a.Hq / a.Hkv;
 
-    const int q0 = a.q_start[b];
-    const int qfull = a.q_start[b + 1] - q0;
+    const int q0 = a.q_start[b], q1 = a.q_start[b + 1];
     const bool reporter = tid == 0 && kv == 0 && blockIdx.x == 0;
-    if (q0 < 0 || qfull < 0 || q0 + qfull > a.T) {  // rows outside q / out: nothing is touched
+    if (q0 < 0 || q1 < q0 || q1 > a.T) {  // rows outside q / out: nothing is touched
         if (reporter) flag_status(a.status, TQ_STATUS_BAD_LEN);
         return;
     }
+    const int qfull = q1 - q0;
     if (qfull > a.max_q_len && reporter) flag_status(a.status, TQ_STATUS_BAD_LEN);
     const int qlen = min(qfull, a.max_q_len);  // a longer chunk is cut: its last rows are not written
     const int rows_b = qlen * G;
@@ -1039,8 +1039,9 @@ __global__ void __launch_bounds__(kRows, VPlan<D>::kCtas) votes_kernel(WArgs a) 
         return blk < a.max_blocks ? (int)ldg_u32(a.block_tables + (size_t)b * a.max_blocks + blk) : -1;
     };
     int blk = block_of(blockIdx.x);
-    const int q0 = a.q_start[b], qfull = a.q_start[b + 1] - q0;
-    if (q0 < 0 || qfull <= 0 || q0 + qfull > a.T) return;  // flagged by the attention kernel
+    const int q0 = a.q_start[b], q1 = a.q_start[b + 1];
+    if (q0 < 0 || q1 <= q0 || q1 > a.T) return;  // flagged by the attention kernel
+    const int qfull = q1 - q0;
     const int qlen = min(qfull, a.max_q_len);
     const int L = a.seq_lens[b];
     if (L < qfull || L > a.max_blocks * kBlock) return;

@@ -247,3 +247,26 @@ def test_queries_at_the_limit_of_fp16(tq, orc, kind, call):
     assert torch.equal(out2.cpu()[keep], out.cpu()[keep]) and torch.isfinite(tw2).all()
     # a row's weights sum to 1 as closely as each of them is good
     assert torch.allclose(tw2.sum(-1)[0].cpu(), torch.tensor([n * G - 1.0, n * G]), rtol=float(tol(np.float64(1.0))))
+
+
+# ------------------------------------------------------------------ chunks outside the rows
+@pytest.mark.parametrize("weights", [False, True])
+def test_prefill_chunks_outside_the_rows_touch_nothing(tq, orc, weights):
+    """Row offsets that no chunk can have, those whose difference leaves 32 bits among them: the
+    status, and neither out nor the sums are touched."""
+    Hkv, G, L, d, n = 2, 4, 100, 128, 10
+    rng = np.random.default_rng(1)
+    s = Seq(tq, orc, _bf16(rng.standard_normal((L, Hkv, d))), _bf16(rng.standard_normal((L, Hkv, d))))
+    q = _bf16(rng.standard_normal((n, Hkv * G, d))).cuda()
+    low, high = -2 ** 31, 2 ** 31 - 1
+    for a, b in [(5, low), (9, low + 3), (low, 5), (-1, 5), (6, 5), (0, n + 1), (5, high), (high, low), (high, high)]:
+        out = torch.full((n, Hkv * G, d), 7.0, device="cuda")
+        tw = torch.full((1, Hkv, L), 3.0, device="cuda")
+        st = _status()
+        qs = _cuda(np.array([a, b], np.int32))
+        if weights:
+            tq.prefill_attention_weights(q, s.cache, s.bt, s.lens, *qs, n, d ** -0.5, tw, out=out, status=st)
+        else:
+            tq.prefill_attention(q, s.cache, s.bt, s.lens, *qs, n, d ** -0.5, out=out, status=st)
+        assert int(st.item()) == tq.STATUS_BAD_LEN, (a, b)
+        assert torch.all(out == 7.0) and torch.all(tw == 3.0), (a, b)
