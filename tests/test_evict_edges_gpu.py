@@ -270,3 +270,92 @@ def test_prefill_chunks_outside_the_rows_touch_nothing(tq, orc, weights):
             tq.prefill_attention(q, s.cache, s.bt, s.lens, *qs, n, d ** -0.5, out=out, status=st)
         assert int(st.item()) == tq.STATUS_BAD_LEN, (a, b)
         assert torch.all(out == 7.0) and torch.all(tw == 3.0), (a, b)
+
+
+# ------------------------------------------------------------------ long contexts
+def _long_reference(q, K, V, scale, window):
+    """weights_reference of one sequence's last rows, in 64 bits on the device."""
+    n, Hq, d = q.shape
+    L, Hkv = K.shape[:2]
+    K, V = (torch.from_numpy(x).cuda() for x in (K, V))
+    q = q.cuda().double()
+    out, w = torch.zeros((n, Hq, d), dtype=torch.float64), torch.zeros((Hkv, L), dtype=torch.float64)
+    hidden = torch.ones((n, L), dtype=torch.bool, device="cuda").triu(L - n + 1)
+    for h in range(Hq):
+        kv = h // (Hq // Hkv)
+        p = torch.softmax((q[:, h] @ K[:, kv].T * scale).masked_fill(hidden, -np.inf), 1)
+        out[:, h] = (p @ V[:, kv]).cpu()
+        w[kv] += p[max(0, n - window):].sum(0).cpu()
+    return out.numpy(), w.numpy()
+
+
+@pytest.mark.parametrize("kind,d,num_splits", [("tq", 128, 0), ("tq", 128, 1), ("tq", 64, 0), ("unrotated", 64, 3),
+                                               ("bf16", 128, 1), ("bf16", 64, 0)])
+def test_decode_weights_over_a_long_context(tq, orc, kind, d, num_splits):
+    """65536 tokens, where sums cut towards zero at every tensor-core step show.
+
+    The output is near sqrt(e / L) = 0.0064 a dim (for weights that sum to 1).  Independent
+    errors of the weights average as the weights themselves: their share of it is the rms of
+    a weight's relative error, a score of rms 1.4 cut by 2^-24 in each of 16 steps, 2^-20 at
+    most.  What does not average are the zero-point sums, 0.13 against codes of the opposite
+    sign (the middle of 32 normal values, 4.14 / 30): a record's product cut by up to 2^-23,
+    0.13 / 0.0064 x 2^-23 = 2.4e-6, and the rounded additions of 683 records a warp (one
+    split, six warps), twice, sqrt(2) 2^-25 0.13 / 0.0064 sqrt(683 / 9 / 6) = 3e-6.  (Summed on
+    in the accumulators, 683 steps cut by 2^-24: 4e-5 x 0.13 / 0.0064 = 8e-4.)  bf16 values
+    have no such pair of sums; theirs are 2^-25 sqrt(1024) = 1e-6 (summed on, 2048 steps cut
+    by 2^-24: 1.2e-4)."""
+    L, G = 65536, 4
+    rng = np.random.default_rng(L + d)
+    s = Seq(tq, orc, _bf16(rng.standard_normal((L, 1, d))), _bf16(rng.standard_normal((L, 1, d))), kind)
+    q = _bf16(rng.standard_normal((1, G, d)))
+    tw = torch.zeros((1, 1, L), device="cuda")
+    out = tq.decode_attention_weights(q.cuda(), s.cache, s.bt, s.lens, L, d ** -0.5, tw, num_splits=num_splits)
+    want, add = _long_reference(q, s.K[0], s.V[0], d ** -0.5, 1)
+    err = np.linalg.norm(out.cpu().numpy() - want) / np.linalg.norm(want)
+    assert err <= 1e-5, err
+    tol = weight_tolerance(q.double().numpy(), s.K, [L], d ** -0.5, 0.0, G)
+    check_weights(tw[0].cpu().numpy(), add, tol(add))
+
+
+@pytest.mark.parametrize("d,Hkv,L,n", [(128, 1, 32768, 5), (64, 8, 16384, 600)])
+def test_prefill_weights_over_a_long_context(tq, orc, d, Hkv, L, n):
+    """Contexts cut into parts (few rows) and whole.  The values' sums have no large partner, so
+    the output's error is that of the weights, 2^-20 at most as in the decode, and of the sums
+    over up to 512 steps, 2^-25 sqrt(512) = 7e-7.  (Summed on in tensor memory, 256 steps of 12
+    products cut by 2^-24: 1.8e-4 of the sum at the end.)"""
+    G = 4
+    rng = np.random.default_rng(L + n)
+    K, V = (_bf16(rng.standard_normal((L, 1, d))).expand(L, Hkv, d).contiguous() for _ in range(2))
+    s = Seq(tq, orc, K, V)
+    q = _bf16(rng.standard_normal((n, Hkv * G, d)))
+    tw = torch.zeros((1, Hkv, L), device="cuda")
+    out = tq.prefill_attention_weights(q.cuda(), s.cache, s.bt, s.lens, *_cuda(np.array([0, n], np.int32)), n,
+                                       d ** -0.5, tw, window=3)
+    want, add = _long_reference(q, s.K[0], s.V[0], d ** -0.5, 3)
+    err = np.linalg.norm(out.cpu().numpy() - want) / np.linalg.norm(want)
+    assert err <= 1e-5, err
+    tol = weight_tolerance(q.double().numpy(), s.K, [L], d ** -0.5, 0.0, 3 * G)
+    check_weights(tw[0].cpu().numpy(), add, tol(add))
+
+
+@pytest.mark.parametrize("kind,max_len,attended", [("tq", 208, 208), ("tq", 200, 208), ("bf16", 200, 200)])
+def test_decode_weights_of_a_length_beyond_the_maximum(tq, orc, kind, max_len, attended):
+    """The sequence is cut as the plain decode cuts it (the 4-bit caches at a whole block), and
+    sums at or past max_seq_len keep their values."""
+    Hkv, G, L, d = 2, 4, 400, 128
+    rng = np.random.default_rng(7)
+    s = Seq(tq, orc, _bf16(rng.standard_normal((L, Hkv, d))), _bf16(rng.standard_normal((L, Hkv, d))), kind)
+    q = _bf16(rng.standard_normal((1, Hkv * G, d)))
+    before = rng.random((1, Hkv, L)).astype(np.float32)
+    tw = torch.from_numpy(before).cuda()
+    st = _status()
+    out = tq.decode_attention_weights(q.cuda(), s.cache, s.bt, s.lens, max_len, d ** -0.5, tw, status=st)
+    assert int(st.item()) == tq.STATUS_BAD_LEN
+    qd = q.double().numpy()
+    want, add = weights_reference(qd, s.K, s.V, [attended], d ** -0.5)
+    check_attention(out.cpu().numpy(), want)
+    got = tw.cpu().numpy()
+    assert np.array_equal(got[..., max_len:], before[..., max_len:])
+    old = before[..., :max_len].astype(np.float64)
+    tol = weight_tolerance(qd, s.K, [attended], d ** -0.5, old, G)
+    check_weights(got[..., :max_len], old + add[..., :max_len], tol(add[..., :max_len]))
