@@ -378,7 +378,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(PrefillArgs a) {
             for (int j = 0; j < 16; j++) x[c0 + j] = t16[j];
         }
         const bool whole = kStep * (s + 1) <= lim;  // the row sees every token of the step
-        if (__all_sync(kFull, whole)) {  // no mask: the norms by packed multiplies
+        const bool gaps = (int)(idv.x | idv.y | idv.z | idv.w) < 0;  // not every block is there
+        if (__all_sync(kFull, whole) && !gaps) {  // no mask: the norms by packed multiplies
 #pragma unroll
             for (int c0 = 0; c0 < kStep; c0 += 4) {
                 const uint4 nw = ld_s128(sNorm + 4 * c0);
@@ -400,7 +401,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(PrefillArgs a) {
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
                     const int t = kStep * s + c0 + j;
-                    x[c0 + j] = whole || t < lim ? x[c0 + j] * nn[j] : -INFINITY;
+                    const bool seen = (whole || t < lim) && id_of(c0 >> 4) >= 0;
+                    x[c0 + j] = seen ? x[c0 + j] * nn[j] : -INFINITY;
                 }
             }
         }

@@ -359,3 +359,27 @@ def test_decode_weights_of_a_length_beyond_the_maximum(tq, orc, kind, max_len, a
     old = before[..., :max_len].astype(np.float64)
     tol = weight_tolerance(qd, s.K, [attended], d ** -0.5, old, G)
     check_weights(got[..., :max_len], old + add[..., :max_len], tol(add[..., :max_len]))
+
+
+@pytest.mark.parametrize("d,Hkv,G,L,n,bad", [
+    (128, 2, 4, 400, 30, [3, 24]),
+    (128, 2, 4, 400, 30, [0, 1, 2, 3]),
+    (64, 2, 8, 500, 100, [30, 31]),
+    (128, 1, 4, 64, 64, [0]),
+    (64, 1, 3, 200, 20, list(range(13))),
+])
+def test_prefill_leaves_absent_blocks_out(tq, orc, d, Hkv, G, L, n, bad):
+    """The same of the prefill without weights."""
+    rng = np.random.default_rng(L + len(bad))
+    s = Seq(tq, orc, _bf16(rng.standard_normal((L, Hkv, d))), _bf16(rng.standard_normal((L, Hkv, d))))
+    bt = s.bt.clone()
+    bt[0, bad] = torch.tensor([-1 if i % 2 else s.cache.num_blocks for i in bad], dtype=torch.int32, device="cuda")
+    there = np.ones(L, bool)
+    for i in bad:
+        there[16 * i:16 * i + 16] = False
+    q = _bf16(rng.standard_normal((n, Hkv * G, d)))
+    st = _status()
+    out = tq.prefill_attention(q.cuda(), s.cache, bt, s.lens, *_cuda(np.array([0, n], np.int32)), n, d ** -0.5, status=st)
+    assert int(st.item()) == tq.STATUS_BAD_BLOCK
+    want, _ = _chunk_reference(q.double().numpy(), s.K[0], s.V[0], L, d ** -0.5, 0, there)
+    check_attention(out.cpu().numpy(), want)
