@@ -22,6 +22,9 @@ __device__ __forceinline__ uint4 ld_s128(uint32_t a) {
 __device__ __forceinline__ void st_s32(uint32_t a, uint32_t v) {
     asm volatile("st.shared.b32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
+__device__ __forceinline__ void st_s8(uint32_t a, uint32_t v) {
+    asm volatile("st.shared.b8 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
 __device__ __forceinline__ void st_s64(uint32_t a, uint32_t x, uint32_t y) {
     asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(a), "r"(x), "r"(y) : "memory");
 }

@@ -19,7 +19,9 @@
 //      accumulator is rescaled only when the row maximum grows by more than
 //      2^8), and writes p as fp16 high and low parts;
 //   5. one thread issues O += [p_hi | p_hi | p_lo] . [v_hi ; v_lo ; v_hi]
-//      (M 128, N d, K 3 x 64) into tensor memory.
+//      (M 128, N d, K 3 x 64) into tensor memory; a record with values past fp16 (n s + z
+//      reaches 16 times the largest of its fields) holds them at a sixteenth, and its
+//      products are added sixteen times.
 // Every operand the tensor cores see is exact fp16 except the value and weight
 // splits (22 significant bits each), so the output carries ~2^-21 relative
 // error against the fp64 attention over the same dequantised K/V.
@@ -39,6 +41,7 @@ constexpr int kRows = 128;      // query rows per tile (the M of every MMA)
 constexpr int kStep = 64;       // cached tokens per step (four blocks; the N of S)
 constexpr int kThreads = 128;   // one thread per query row
 constexpr int kRecStages = 2;   // steps whose records are in flight
+constexpr int kAgain = 16;      // products of a record whose values are held at a sixteenth
 
 // ------------------------------------------------------------------ shared memory plan
 // All operand tiles use the no-swizzle core-matrix layout: a core matrix is 8
@@ -60,6 +63,7 @@ struct PPlan {
     static constexpr uint32_t kIds = kNorm + kStep * 4u;
     static constexpr uint32_t kBars = kIds + kRecStages * 16u;  // record stages, S, O
     static constexpr uint32_t kMisc = kBars + (kRecStages + 2) * 8u;  // tensor-memory base, abort flag
+    static constexpr uint32_t kSmall = kMisc + 8u;  // a byte per record: its values at a sixteenth
     static constexpr uint32_t kEnd = kMisc + 16u;
     static constexpr uint32_t kCols = D == 128 ? 256u : 128u;  // S (64 columns) + O (d columns)
     static_assert(kRec % 16 == 0 && Rec<D>::kBytes % 16 == 0, "bulk copies need 16-byte alignment");
@@ -92,6 +96,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(PrefillArgs a) {
     extern __shared__ __align__(1024) unsigned char psm[];
     const uint32_t base = saddr(psm);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    static_assert(PL::kSmall % 4 == 0 && PL::kSmall + 4 <= PL::kEnd, "a word of record bytes");
     const int b = blockIdx.z, kv = blockIdx.y, tile = blockIdx.x;
     const int G = a.Hq / a.Hkv;
 
@@ -290,41 +295,48 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(PrefillArgs a) {
             st_s128(sK + (uint32_t)((tt / 8) * (16 * D) + c * 128 + (tt % 8) * 16), w4);
         }
         // ---- values: token tt, byte row r of its pair chunk -> columns (D/8) r ..
-        // (D/8) r + D/8 - 1 (dims 16m + 2r + e), high and low parts
-#pragma unroll 1
-        for (int u = tid; u < kStep * 8; u += kThreads) {
-            const int tt = u % kStep, r = u / kStep;  // consecutive tokens: bank-free stores
-            const int j = tt >> 4, o = tt & 15;
-            const bool valid = id_of(j) >= 0 && kStep * s + tt < maxlim;
-            float v[D / 8];
+        // (D/8) r + D/8 - 1 (dims 16m + 2r + e), high and low parts.  A thread's token is the
+        // same in every turn (consecutive tokens: bank-free stores)
+        static_assert(kThreads % kStep == 0, "one token per thread");
+        const int tt = tid % kStep, o = tt & 15;
+        const uint32_t rec = st + (uint32_t)(tt >> 4) * REC;
+        const bool valid = id_of(tt >> 4) >= 0 && kStep * s + tt < maxlim;
+        float sc[D / 32], zr[D / 32];
+        float most = 0.f;  // the token's largest value
+#pragma unroll
+        for (int g = 0; g < D / 32; g++) {
+            sc[g] = zr[g] = 0.f;
             if (valid) {
-                const uint32_t rec = st + (uint32_t)j * REC;
-                const uint32_t ch =
-                    rec + R::kVCodes + (uint32_t)((8 * (o >> 1) + ((r + 2 * (o >> 1)) & 7)) * (D / 8));
-                float sc[D / 32], zr[D / 32];
+                const uint32_t gp = (uint32_t)R::group_pos(o, g);
+                const uint32_t sw = ld_s32(rec + R::kVScale + (gp & ~3u));
+                const uint32_t zw = ld_s32(rec + R::kVZero + (gp & ~3u));
+                sc[g] = half_bits_to_float((uint16_t)(sw >> (8 * (gp & 2))));
+                zr[g] = half_bits_to_float((uint16_t)(zw >> (8 * (gp & 2))));
+                most = fmaxf(most, fmaxf(fabsf(zr[g]), fabsf(fmaf(15.f, sc[g], zr[g]))));
+            }
+        }
+        // do values of the record (this lane's half of the warp) pass fp16?
+        const bool small = (__ballot_sync(kFull, most > 65504.f) >> (lane & 16) & 0xffffu) != 0;
+        if (tid < kStep && o == 0) st_s8(base + PL::kSmall + (uint32_t)(tt >> 4), small);
+        if (small) {
 #pragma unroll
-                for (int g = 0; g < D / 32; g++) {
-                    const uint32_t gp = (uint32_t)R::group_pos(o, g);
-                    const uint32_t sw = ld_s32(rec + R::kVScale + (gp & ~3u));
-                    const uint32_t zw = ld_s32(rec + R::kVZero + (gp & ~3u));
-                    sc[g] = half_bits_to_float((uint16_t)(sw >> (8 * (gp & 2))));
-                    zr[g] = half_bits_to_float((uint16_t)(zw >> (8 * (gp & 2))));
+            for (int g = 0; g < D / 32; g++) sc[g] *= 1.f / kAgain, zr[g] *= 1.f / kAgain;
+        }
+#pragma unroll 1
+        for (int r = tid / kStep; r < 8; r += kThreads / kStep) {
+            float v[D / 8];
+            const uint32_t ch = rec + R::kVCodes + (uint32_t)((8 * (o >> 1) + ((r + 2 * (o >> 1)) & 7)) * (D / 8));
+#pragma unroll
+            for (int q = 0; q < D / 32; q++) {  // word q: bytes of m = 2q, 2q + 1 of both tokens
+                const uint32_t w = ld_s32(ch + 4 * q) >> (16 * (o & 1));
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                    const int m = 2 * q + e;
+                    const uint32_t byte = (w >> (8 * e)) & 0xFFu;
+                    const int g = m >> 1;
+                    v[2 * m] = fmaf((float)(byte & 15u), sc[g], zr[g]);
+                    v[2 * m + 1] = fmaf((float)(byte >> 4), sc[g], zr[g]);
                 }
-#pragma unroll
-                for (int q = 0; q < D / 32; q++) {  // word q: bytes of m = 2q, 2q + 1 of both tokens
-                    const uint32_t w = ld_s32(ch + 4 * q) >> (16 * (o & 1));
-#pragma unroll
-                    for (int e = 0; e < 2; e++) {
-                        const int m = 2 * q + e;
-                        const uint32_t byte = (w >> (8 * e)) & 0xFFu;
-                        const int g = m >> 1;
-                        v[2 * m] = fmaf((float)(byte & 15u), sc[g], zr[g]);
-                        v[2 * m + 1] = fmaf((float)(byte >> 4), sc[g], zr[g]);
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < D / 8; e++) v[e] = 0.f;
             }
 #pragma unroll
             for (int n8 = 0; n8 < D / 64; n8++) {  // one 8-column group: 16 bytes of each part
@@ -474,17 +486,21 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(PrefillArgs a) {
         // ---- O += [p_hi | p_hi | p_lo] [v_hi ; v_lo ; v_hi] (thread 0)
         if (tid == 0) {
             constexpr uint32_t idO = idesc_f16(kRows, D, 1);
+            auto product = [&](int seg, int ks, uint32_t acc) {
+                const uint64_t ad = mdesc(sP + (seg == 2 ? 16384u : 0u) + 256u * ks, 128, 1024);
+                const uint64_t bd = mdesc(sV + (seg == 1 ? 128u * D : 0u) + 256u * ks, 128, 1024);
+                mma_f16(tO, ad, bd, idO, acc);
+            };
 #pragma unroll 1
-            for (int seg = 0; seg < 3; seg++) {
-                const uint32_t pa = sP + (seg == 2 ? 16384u : 0u);
-                const uint32_t vb = sV + (seg == 1 ? 128u * D : 0u);
+            for (int seg = 0; seg < 3; seg++)
 #pragma unroll 1
-                for (int ks = 0; ks < kStep / 16; ks++) {
-                    const uint64_t ad = mdesc(pa + 256u * ks, 128, 1024);
-                    const uint64_t bd = mdesc(vb + 256u * ks, 128, 1024);
-                    mma_f16(tO, ad, bd, idO, (o_issued > 0 || seg > 0 || ks > 0) ? 1u : 0u);
-                }
-            }
+                for (int ks = 0; ks < kStep / 16; ks++) product(seg, ks, o_issued > 0 || seg > 0 || ks > 0);
+            // a record (step ks) that holds a sixteenth, fifteen times more
+            const uint32_t small_recs = ld_s32(base + PL::kSmall);
+            if (small_recs)
+#pragma unroll 1
+                for (int i = 0; i < 3 * (kAgain - 1) * (kStep / 16); i++)
+                    if (const int ks = i / (3 * (kAgain - 1)); (small_recs >> (8 * ks)) & 1u) product(i % 3, ks, 1);
             mma_commit(barO);
         }
         o_started = true;

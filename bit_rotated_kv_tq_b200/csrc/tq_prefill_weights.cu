@@ -79,9 +79,6 @@ __device__ __forceinline__ uint2 ld_s64(uint32_t a) {
 }
 // bits 0 .. n - 1
 __device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? ~0u : n > 0 ? (1u << n) - 1u : 0u; }
-__device__ __forceinline__ void st_s8(uint32_t a, uint32_t v) {
-    asm volatile("st.shared.b8 [%0], %1;" ::"r"(a), "r"(v) : "memory");
-}
 // Whether a thread of two warps says so; a barrier of theirs (id)
 __device__ __forceinline__ bool pair_any(uint32_t id, bool yes) {
     uint32_t r;

@@ -383,3 +383,40 @@ def test_prefill_leaves_absent_blocks_out(tq, orc, d, Hkv, G, L, n, bad):
     assert int(st.item()) == tq.STATUS_BAD_BLOCK
     want, _ = _chunk_reference(q.double().numpy(), s.K[0], s.V[0], L, d ** -0.5, 0, there)
     check_attention(out.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("d,L,n,spans", [
+    (128, 600, 40, [(100, 101, 0.0, 7e4), (333, 340, -3e4, 9e4)]),
+    (128, 600, 40, [(0, 600, 0.0, 7e4)]),
+    (64, 700, 130, [(695, 700, -6e4, 6e4)]),
+    (64, 700, 130, [(64, 128, 0.0, 9e5), (300, 301, -6.4e4, 9e5)]),
+])
+def test_prefill_value_ranges(tq, orc, d, L, n, spans):
+    """The same of the prefill without weights, which sums on in tensor memory: every one of its
+    products (up to 192 a step) is cut by 2^-23 of the sum so far, and weights of at least
+    the largest's 1 keep 2^-25 in their two parts."""
+    Hkv, G = 2, 4
+    rng = np.random.default_rng(L + d)
+    K = _bf16(rng.standard_normal((L, Hkv, d)))
+    V = rng.standard_normal((L, Hkv, d)).astype(np.float32)
+    for a, b, lo, hi in spans:
+        V[a:b] = rng.uniform(lo, hi, (b - a, Hkv, d))
+        V[a:b, :, :32] = rng.standard_normal((b - a, Hkv, 32))
+        V[a:b, :, 32], V[a:b, :, 33] = lo, hi
+    s = Seq(tq, orc, K, _bf16(V))
+    q = _bf16(rng.standard_normal((n, Hkv * G, d)))
+    qs = np.array([0, n], np.int32)
+    st = _status()
+    out = tq.prefill_attention(q.cuda(), s.cache, s.bt, s.lens, *_cuda(qs), n, d ** -0.5, status=st).cpu().numpy()
+    assert int(st.item()) == 0 and np.isfinite(out).all()
+    qd = q.double().numpy()
+    want, _ = weights_reference(qd, s.K, s.V, [L], d ** -0.5, qs)
+    mean_v = weights_reference(qd, s.K, np.abs(s.V), [L], d ** -0.5, qs)[0]
+    all_v = np.zeros_like(mean_v)
+    for i in range(n):
+        all_v[i] = np.repeat(np.abs(s.V[0, :L - n + i + 1]).sum(0), G, 0)
+    tol = weight_tolerance(qd, s.K, [L], d ** -0.5, 0.0, 0)
+    bound = (tol(np.float64(1.0)) + 3.25 * 2.0 ** -22 + (L / 64 + 1) * 192 * 2.0 ** -23) * mean_v
+    bound += 2.0 ** -25 * all_v + 2.0 ** -21
+    err = np.abs(out - want)
+    assert np.all(err <= bound), float(np.max(err / bound))
