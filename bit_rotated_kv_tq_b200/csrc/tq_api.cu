@@ -505,7 +505,8 @@ TQ_API int tq_decode_attention_weights(const void* q, const tq_cache_t* cache, c
     if (err != TQ_OK || B == 0) return err;
     if (max_blocks > kMaxTable)
         return fail(TQ_ERR_UNSUPPORTED, "tq_decode_attention_weights: max_blocks %d too large", max_blocks);
-    if (!token_weights || weights_stride < max_seq_len)
+    // (rows of no token need no sums: an empty tensor's pointer is null)
+    if ((!token_weights && max_seq_len > 0) || weights_stride < max_seq_len)
         return fail(TQ_ERR_INVALID_ARG,
                     "tq_decode_attention_weights: token_weights required, weights_stride %lld >= max_seq_len %d",
                     (long long)weights_stride, max_seq_len);
@@ -540,7 +541,7 @@ TQ_API int tq_evict_select(const float* token_weights, int64_t weights_stride, c
     if (B > 65535 || H_kv > 32 || max_seq_len > kMaxTokens || budget > kMaxTokens)
         return fail(TQ_ERR_UNSUPPORTED,
                     "tq_evict_select: B %d (<= 65535), H_kv %d (<= 32), max_seq_len and budget (<= 2^30)", B, H_kv);
-    if (!token_weights || !seq_lens || !kept || !kept_lens)
+    if ((!token_weights && max_seq_len > 0) || !seq_lens || !kept || !kept_lens)
         return fail(TQ_ERR_INVALID_ARG, "tq_evict_select: token_weights, seq_lens, kept, kept_lens required");
     if (!aligned(token_weights, 4) || !aligned(seq_lens, 4) || !aligned(kept, 4) || !aligned(kept_lens, 4) ||
         (status && !aligned(status, 4)))

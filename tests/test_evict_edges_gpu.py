@@ -420,3 +420,19 @@ def test_prefill_value_ranges(tq, orc, d, L, n, spans):
     bound += 2.0 ** -25 * all_v + 2.0 ** -21
     err = np.abs(out - want)
     assert np.all(err <= bound), float(np.max(err / bound))
+
+
+# ------------------------------------------------------------------ nothing there yet
+@pytest.mark.parametrize("kind", ["tq", "bf16"])
+def test_sequences_and_sums_of_no_token(tq, orc, kind):
+    """Before the first token: sums of no place, lengths of 0."""
+    cache = tq.Cache(4, 2, 128, bf16=kind == "bf16")
+    bt = torch.zeros((3, 1), dtype=torch.int32, device="cuda")
+    lens = torch.zeros(3, dtype=torch.int32, device="cuda")
+    tw = torch.empty((3, 2, 0), device="cuda")
+    st = _status()
+    q = torch.randn((3, 8, 128), device="cuda").to(torch.bfloat16)
+    out = tq.decode_attention_weights(q, cache, bt, lens, 0, 0.1, tw, status=st)
+    kept, n = tq.evict_select(tw, lens, 0, 5, sink=1, recent=1, status=st)
+    tq.compact_cache(cache, bt, lens, kept, n, status=st)
+    assert int(st.item()) == 0 and torch.all(out == 0) and torch.all(kept == -1) and torch.all(n == 0)
