@@ -436,3 +436,38 @@ def test_sequences_and_sums_of_no_token(tq, orc, kind):
     kept, n = tq.evict_select(tw, lens, 0, 5, sink=1, recent=1, status=st)
     tq.compact_cache(cache, bt, lens, kept, n, status=st)
     assert int(st.item()) == 0 and torch.all(out == 0) and torch.all(kept == -1) and torch.all(n == 0)
+
+
+# ------------------------------------------------------------------ captured and replayed
+@pytest.mark.parametrize("L,n", [(3000, 5), (400, 300)])
+def test_prefill_weights_in_a_graph(tq, orc, L, n):
+    """Captured once, replayed with other lengths and queries: what the calls give one by one."""
+    Hkv, G, d = 8, 4, 64
+    rng = np.random.default_rng(L)
+    s = Seq(tq, orc, _bf16(rng.standard_normal((L, Hkv, d))), _bf16(rng.standard_normal((L, Hkv, d))))
+    q = torch.empty((n, Hkv * G, d), dtype=torch.bfloat16, device="cuda")
+    qs = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    ws = torch.empty(tq.prefill_weights_workspace_bytes(1, Hkv * G, Hkv, d, n, 3), dtype=torch.uint8, device="cuda")
+    out, tw = torch.empty((n, Hkv * G, d), device="cuda"), torch.empty((1, Hkv, L), device="cuda")
+
+    def call(q, lens, qs, out, tw, ws=None):
+        tq.prefill_attention_weights(q, s.cache, s.bt, lens, qs, n, d ** -0.5, tw, window=3, out=out, workspace=ws)
+
+    lens = s.lens.clone()
+    call(q.zero_(), lens, qs, out, tw.zero_(), ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(q, lens, qs, out, tw, ws)
+    for length, rows in ((L, n), (L - 77, n), (L, n - 4), (n, n)):
+        q.copy_(_bf16(rng.standard_normal(tuple(q.shape))))
+        lens.fill_(length)
+        qs[1] = rows
+        start = torch.rand_like(tw)
+        want, sums = torch.full_like(out, 7.0), start.clone()
+        call(q, lens, qs, want, sums)
+        tw.copy_(start)
+        out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(tw, sums)
