@@ -12,7 +12,7 @@
 //                   tokens
 //   warps 13-15     the keys, as fp16 centroids (exact)
 //   warp 12         issues the MMAs: S = q~ C^T with the query's two fp16 parts along K,
-//                   O = [p_hi | p_hi | p_lo] [v_hi ; v_lo ; v_hi] with p from tensor memory
+//                   O = [p_lo | p_hi | p_hi] [v_hi ; v_lo ; v_hi] with p from tensor memory
 // The scores of step s + 1 are formed while step s is in its softmax, and the product of
 // step s while step s + 1 is: two score buffers per tile, two stages of operands.
 //
@@ -869,9 +869,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_rows_kernel(WArgs a) {
             auto scores = [&](uint32_t st, int tile) {
                 const uint64_t a = dq + (uint64_t)tile * (512 * D / 16), b = dk + (uint64_t)st * (PL::kKStage / 16);
                 const uint32_t d = tm + (uint32_t)tile * kTileCols + st * kStep;
+                // (the queries' low parts first: a sum is cut by what it is when a product joins it)
 #pragma unroll
                 for (int ks = 0; ks < 2 * D / 16; ks++)
-                    mma_ss(el, d, a + 16 * ks, b + 16 * (ks % (D / 16)), idS, ks > 0);
+                    mma_ss(el, d, a + 16 * (ks ^ (D / 16)), b + 16 * (ks % (D / 16)), idS, ks > 0);
                 commit(el, bar(B_SFULL + 2 * tile + st));
             };
             wait(B_QFULL, 0);
@@ -918,12 +919,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_rows_kernel(WArgs a) {
                     tc_after_sync();
                     const uint32_t tb = tm + (uint32_t)t * kTileCols, pa = tb + st * kStep;
                     const uint64_t b = dv + (uint64_t)st * (PL::kVStage / 16);
+                    // (p_hi v_lo and p_lo v_hi before the large products)
 #pragma unroll
-                    for (int seg = 0; seg < 3; seg++)
+                    for (int seg = 2; seg >= 0; seg--)
 #pragma unroll
                         for (int ks = 0; ks < kStep / 16; ks++)
                             mma_ts(el, tb + kOCol, pa + 16u * ks + (seg == 2 ? 8u : 0u),
-                                   b + (seg == 1 ? PL::kVPart / 16 : 0u) + 16 * ks, idO, seg > 0 || ks > 0);
+                                   b + (seg == 1 ? PL::kVPart / 16 : 0u) + 16 * ks, idO, seg < 2 || ks > 0);
                     // a record that holds a sixteenth, fifteen times more
                     const uint32_t small = ld_s32(sSmall + 4 * st);
                     if (__any_sync(kFull, small != 0)) {
@@ -1174,7 +1176,7 @@ __global__ void __launch_bounds__(kRows, VPlan<D>::kCtas) votes_kernel(WArgs a) 
                 const uint32_t el = elect_one(), tm = __shfl_sync(kFull, tmem, 0);
 #pragma unroll
                 for (int ks = 0; ks < 2 * D / 16; ks++)
-                    mma_ss(el, tm, dk + 16 * (ks % (D / 16)), dq + 16 * ks, id, ks > 0);
+                    mma_ss(el, tm, dk + 16 * (ks % (D / 16)), dq + 16 * (ks ^ (D / 16)), id, ks > 0);
                 commit(el, barS);
             }
             ok = bar_wait(barS, products++ & 1u);

@@ -471,3 +471,22 @@ def test_prefill_weights_in_a_graph(tq, orc, L, n):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want) and torch.equal(tw, sums)
+
+
+@pytest.mark.parametrize("d,L,n", [(128, 1290, 10), (64, 1290, 100)])
+def test_prefill_weights_add_small_products_first(tq, orc, d, L, n):
+    """A tensor-core step cuts its sum by 2^-24 of it on average.  A score (rms 1.44, base 2)
+    takes its d / 16 <= 8 large products behind the small ones, 8 x 2^-24 x 1.44 ln 2 =
+    4.8e-7 of a weight, a step's output its four, 2.4e-7; the query's parts (2^-23) and the
+    exponential (2 ulp) add 2.4e-7.  (Large products first: 16 and 12 such cuts, 1.7e-6.)"""
+    Hkv, G = 4, 4
+    rng = np.random.default_rng(L + d)
+    s = Seq(tq, orc, _bf16(rng.standard_normal((L, Hkv, d))), _bf16(rng.standard_normal((L, Hkv, d))))
+    q = _bf16(rng.standard_normal((n, Hkv * G, d)))
+    qs = np.array([0, n], np.int32)
+    tw = torch.zeros((1, Hkv, L), device="cuda")
+    out = tq.prefill_attention_weights(q.cuda(), s.cache, s.bt, s.lens, *_cuda(qs), n, d ** -0.5, tw, window=1)
+    want, add = weights_reference(q.double().numpy(), s.K, s.V, [L], d ** -0.5, qs, 1)
+    for got, ref in ((out, want), (tw, add)):
+        err = np.linalg.norm(got.cpu().numpy() - ref) / np.linalg.norm(ref)
+        assert err <= 1e-6, err
