@@ -72,13 +72,6 @@ __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
 __device__ __forceinline__ void bar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ uint2 ld_s64(uint32_t a) {
-    uint2 v;
-    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-    return v;
-}
-// bits 0 .. n - 1
-__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? ~0u : n > 0 ? (1u << n) - 1u : 0u; }
 // Whether a thread of two warps says so; a barrier of theirs (id)
 __device__ __forceinline__ bool pair_any(uint32_t id, bool yes) {
     uint32_t r;
@@ -330,8 +323,7 @@ struct APlan {
     static constexpr uint32_t kBars = kNorm + 4u * 4u * kStep;
     static constexpr uint32_t kMisc = kBars + 32u * 8u;  // tensor-memory base, abort flag, part, parts
     static constexpr uint32_t kSmall = kMisc + 16u;      // two stages: a byte per record, its values at a sixteenth
-    static constexpr uint32_t kThere = kSmall + 16u;     // D = 64, four steps: bit t: token t is there
-    static constexpr uint32_t kEnd = kThere + 32u;
+    static constexpr uint32_t kEnd = kSmall + 16u;
     static_assert(kEnd <= 232448u, "227 KB per CTA");
 };
 // Barriers.  Step s is phase s / 2 of the ones kept per stage, s / 4 of NORM, s of the rest.
@@ -394,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_rows_kernel(WArgs a) {
 
     const uint32_t sQ = base + PL::kQ, sK = base + PL::kK, sV = base + PL::kV;
     const uint32_t sLut = base + PL::kLut, sNorm = base + PL::kNorm, bars = base + PL::kBars;
-    const uint32_t sSmall = base + PL::kSmall, sThere = base + PL::kThere;
+    const uint32_t sSmall = base + PL::kSmall;
     volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(psm + PL::kMisc);
     auto bar = [&](uint32_t id) { return bars + 8 * id; };
 
@@ -469,7 +461,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_rows_kernel(WArgs a) {
         const int R_ = row0 + tile * kRows + (tid & 127);  // this thread's row
         const bool row_ok = R_ < rows_b;
         const int ri = R_ / G, rh = R_ % G;
-        const int lim = row_ok && L >= 0 ? L - qfull + ri + 1 - kStep * step0 : 0;  // it sees positions < lim
+        // it sees positions < lim; a row that is not there sees all, so that its warp takes no masks
+        // for it (what it gives is not used)
+        const int lim = row_ok ? L - qfull + ri + 1 - kStep * step0 : 0x7fffffff;
         const uint32_t tT = tmem + (uint32_t)tile * kTileCols + ((uint32_t)(32 * (warp & 3)) << 16);
         float o[D];
 #pragma unroll
@@ -516,15 +510,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_rows_kernel(WArgs a) {
                 // 16 tokens in flight at a time; at D = 64 there are registers for all 64,
                 // which then are read and scaled once
                 constexpr bool KEEP = D == 64;
-                // what the row sees: a bit a token, or where registers are short the limit and the
-                // norm of each (d 64: bits 300 us on 16 x 512 tokens at 4096, the other way 311;
-                // d 128: bits 2.74 ms on 2048 at 32768, the other way 2.60)
-                uint32_t see[2];
-                if constexpr (MASK && KEEP) {
-                    const uint2 there = ld_s64(sThere + 8u * (uint32_t)(s & 3));
-                    see[0] = there.x & low_bits(lim - kStep * s);
-                    see[1] = there.y & low_bits(lim - kStep * s - 32);
-                }
                 // scores 16 c + j .. + 3 times their norms, plus add
                 auto four = [&](const float* xc, int c, int j, float2 add, float2& y, float2& z) {
                     const uint4 nw = ld_s128(nrm + 64u * c + 4u * j);
@@ -532,13 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_rows_kernel(WArgs a) {
                                    make_float2(__uint_as_float(nw.x), __uint_as_float(nw.y)), add);
                     z = __ffma2_rn(make_float2(xc[2], xc[3]),
                                    make_float2(__uint_as_float(nw.z), __uint_as_float(nw.w)), add);
-                    if constexpr (MASK && KEEP) {
-                        const uint32_t b = see[c >> 1] >> (16 * (c & 1) + j);
-                        y.x = b & 1u ? y.x : -INFINITY;
-                        y.y = b & 2u ? y.y : -INFINITY;
-                        z.x = b & 4u ? z.x : -INFINITY;
-                        z.y = b & 8u ? z.y : -INFINITY;
-                    } else if constexpr (MASK) {
+                    if constexpr (MASK) {
                         const int t = kStep * s + 16 * c + j;
                         y.x = t < lim && nw.x != kAbsent ? y.x : -INFINITY;
                         y.y = t + 1 < lim && nw.y != kAbsent ? y.y : -INFINITY;
@@ -835,10 +814,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_rows_kernel(WArgs a) {
                     }
                 }
                 if (job0 < 64) {  // (behind the last token the field may hold anything)
-                    if constexpr (D == 64) {
-                        const uint32_t there = __ballot_sync(kFull, there0);
-                        if (lane == 0) st_s32(sThere + 8u * (uint32_t)(s & 3) + 4u * (uint32_t)(warp - 13), there);
-                    }
                     const float norm = kStep * s + job0 < maxlim ? half_bits_to_float(kn) : 0.f;
                     st_s32(sNorm + (uint32_t)(s & 3) * (4u * kStep) + 4u * job0,
                            there0 ? __float_as_uint(norm) : kAbsent);
