@@ -783,8 +783,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_split_kernel(DecodeArgs
                 sts32(dh + 2 * e, h2u(hp));
                 sts32(dl + 2 * e, h2u(__floats2half2_rn(y0 - hf.x, y1 - hf.y)));
             }
-            // infinite or not a number: no score of the row is one
-            if (W && ((top + 0x04000400u) & 0x80008000u)) flag_status(a.status, TQ_STATUS_RANGE);
+            // infinite or not a number: no score of the row is one (a padded row may hold anything)
+            if (W && cu.L > 0 && ((top + 0x04000400u) & 0x80008000u)) flag_status(a.status, TQ_STATUS_RANGE);
         }
         half_sync(half);
 

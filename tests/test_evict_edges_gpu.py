@@ -249,6 +249,29 @@ def test_queries_at_the_limit_of_fp16(tq, orc, kind, call):
     assert torch.allclose(tw2.sum(-1)[0].cpu(), torch.tensor([n * G - 1.0, n * G]), rtol=float(tol(np.float64(1.0))))
 
 
+@pytest.mark.parametrize("num_splits", [0, 1])
+@pytest.mark.parametrize("kind", ["tq", "bf16"])
+def test_padded_rows_of_a_batch_may_hold_anything(tq, orc, kind, num_splits):
+    """Sequences of no token beside a real one, their queries not numbers: output 0, no status, and
+    sums as they were."""
+    Hkv, G, L, d = 2, 4, 200, 128
+    rng = np.random.default_rng(3)
+    s = Seq(tq, orc, _bf16(rng.standard_normal((L, Hkv, d))), _bf16(rng.standard_normal((L, Hkv, d))), kind)
+    q = _bf16(rng.standard_normal((4, Hkv * G, d))).cuda()
+    alone, tw1 = torch.zeros((1, Hkv, L), device="cuda"), torch.full((4, Hkv, L), 3.0, device="cuda")
+    want = tq.decode_attention_weights(q[2:3].contiguous(), s.cache, s.bt, s.lens, L, d ** -0.5, alone)
+    q[[0, 1, 3]] = float("nan")
+    q[1, 0] = float("inf")
+    lens = torch.tensor([0, 0, L, 0], dtype=torch.int32, device="cuda")
+    bt = torch.full((4, s.bt.shape[1]), -1, dtype=torch.int32, device="cuda")
+    bt[2] = s.bt[0]
+    st = _status()
+    out = tq.decode_attention_weights(q, s.cache, bt, lens, L, d ** -0.5, tw1, num_splits=num_splits, status=st)
+    assert int(st.item()) == 0 and torch.all(out[[0, 1, 3]] == 0) and torch.all(tw1[[0, 1, 3]] == 3.0)
+    check_attention(out[2:3].cpu().numpy(), want.double().cpu().numpy())
+    assert torch.allclose(tw1[2], 3.0 + alone[0], rtol=1e-5)
+
+
 # ------------------------------------------------------------------ chunks outside the rows
 @pytest.mark.parametrize("weights", [False, True])
 def test_prefill_chunks_outside_the_rows_touch_nothing(tq, orc, weights):
