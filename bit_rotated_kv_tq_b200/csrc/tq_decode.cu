@@ -40,7 +40,7 @@
 //
 // With token weights (template parameter W) the same pass also stores every score and sums
 // more exactly (record_values).  On 32 x 8192 tokens (d 128, four heads per kv head) the
-// split kernel then takes 95 us against 66: 428 instructions a record against 326, at the
+// split kernel then takes 96 us against 66: 429 instructions a record against 326, at the
 // same 12 warps per SM; of the difference, leaving the codes uncentred gives back 7 us,
 // summing on in the accumulators 3 us, the score stores 3 us.
 #include <mutex>

@@ -10,8 +10,8 @@
 // first one's through distributed shared memory, and it hands the digit to all.  One more
 // pass judges the keys, and the kept positions leave in order.  The row is read once
 // (8.4 MB of sums: 1.3 us of HBM); what bounds the call is the chain of short phases, each
-// a barrier and a few shared-memory latencies: 14 us for 256 rows of 8192, 25 us for 32 rows
-// of 131072, and from Python the launch (13 us a call).
+// a barrier and a few shared-memory latencies: calls in a row take 16 us for 256 rows of 8192,
+// 27 us for 32 rows of 131072, and 12 us (launch and Python) where that is longer.
 //
 // Compaction.  Kept token j of a (sequence, kv head) moves from slot kept[j] to slot j.
 // One warp builds one destination record (16 tokens): it gathers the 16 source tokens'
@@ -567,9 +567,11 @@ cudaError_t launch_select(const float* w, long long stride, const int32_t* seq_l
                           int budget, int sink, int recent, int32_t* kept, int32_t* kept_lens, int32_t* status,
                           cudaStream_t stream) {
     SelectArgs a = {w, stride, seq_lens, B, Hkv, max_seq_len, budget, sink, recent, kept, kept_lens, status, 0};
-    // the fewest CTAs (up to 8) whose part of a row is judged in one go.  More are slower
-    // where there are rows enough (256 rows x 8192: 18 us with one, 26 with two), fewer
-    // where parts get long (32 rows x 131072: 27 us with eight, 32 with four).
+    // the fewest CTAs (up to 8) whose part of a row is judged in one go.  Calls in a row: more
+    // are slower where there are rows enough (256 rows x 8192: 16.5 us with one, 26.7 with two),
+    // fewer where parts get long (32 rows x 131072: 26.7 us with eight, 28.7 with four, 84 with
+    // two).  Two to eight rows would gain by more: x 16384, 16.5 us with one, 12.4 with four; x
+    // 8192, 12.4 and 10.7 to 12.3.
     int C = 1;
     while (C < 8 && (max_seq_len + C - 1) / C > 32 * kSelThreads) C *= 2;
     const int per = (max_seq_len + C - 1) / C;

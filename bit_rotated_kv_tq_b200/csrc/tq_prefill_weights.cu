@@ -26,13 +26,15 @@
 // Few rows have few CTAs: their contexts are cut into parts, which leave their sums to the
 // CTAs of the second kernel.
 //
-// Measured (2048 tokens at context 32768, 32 query / 8 kv heads, d 128): 2.3-2.6 ms, of which
-// 35 us are the votes; the tensor pipe is active 60 % of the cycles of a resident CTA.  A step
-// takes its row warps about 4000 clocks (maximum 700, weights 1300, product 700, barriers),
-// against 2560 for its MMAs (2.5 times those of a product of single fp16 parts), and a CTA by
-// itself about 10 us; 256 CTAs on 148 SMs leave a seventh of the second wave empty.  With one
-// thread issuing under a branch the MMAs were the bound (5.1 ms), with keys and values in the
-// same warps those were (3.0 ms).
+// Measured (2048 tokens at context 32768, 32 query / 8 kv heads, d 128): 2.6-2.7 ms, of which
+// 35 us are the votes (3.8 ms where all 2048 tokens vote); the tensor pipe is active 60 % of the
+// cycles of a resident CTA.  A step takes its row warps about 4000 clocks (maximum 700, weights
+// 1300, product 700, barriers), against 2560 of MMA arithmetic (2.5 times that of a product of
+// single fp16 parts; near 3070 if the scores' operands, 6 KB of shared memory a K step, are
+// read at 128 bytes a clock), and a CTA by itself about 10 us; 256 CTAs on 148 SMs leave a
+// seventh of the second wave empty.  With one thread issuing under a branch the MMAs were the
+// bound (5.1 ms), with keys and values in the same warps those were (3.0 ms).  At d 128 the
+// compiler spills 200-360 bytes a thread, at d 64 16-110.
 //
 // Votes.  token_weights[b][kv][t] += sum over the voting rows r of 2^(s_r,t - lse_r).  The
 // attention leaves each voting tile's rotated queries and row statistics in the workspace;
@@ -1271,10 +1273,10 @@ static int prefill_vote_tiles(int max_q_len, int window, int G) {
 }
 
 // Parts of every context: as many as fill the SMs once.  A chunk of few rows has few CTAs (5
-// tokens, 32 query / 8 kv heads: eight), whose whole contexts would leave most SMs idle: 1059 us
-// at context 32768 against 138 us in 18 parts; 64 tokens x 8 at 8192: 378 us, in two parts
-// 263 us.  More waves of smaller parts do not pay: a part costs about 10 us by itself, and its
-// sums go through memory (300 tokens x 4 at 2048, 160 CTAs: 194 us, in two parts 206 us).
+// tokens, 32 query / 8 kv heads: eight), whose whole contexts would leave most SMs idle: 900 us
+// a call at context 32768 against 98 in 18 parts; 64 tokens x 8 sequences at 8192: 436 us, in
+// two parts 322.  Smaller parts in more waves do not pay: a part costs about 10 us by itself,
+// and its sums go through memory (the first chunk in 32 parts 115 us, the second in four 331).
 namespace {
 int row_pairs(int max_q_len, int G) { return (int)(((long long)max_q_len * G + 2 * kRows - 1) / (2 * kRows)); }
 int context_parts(int B, int Hkv, int max_q_len, int G) {

@@ -74,7 +74,8 @@ enum {
 /* device status bits */
 enum {
     TQ_STATUS_BAD_SLOT = 1,  /* append: slot or logical slot outside the cache / table */
-    TQ_STATUS_BAD_BLOCK = 2, /* a block-table entry outside [0, num_blocks) */
+    TQ_STATUS_BAD_BLOCK = 2, /* a block-table entry outside [0, num_blocks): its tokens take
+                                no part in the attention */
     TQ_STATUS_RANGE = 4,     /* append: a key norm or value scale/zero overflowed fp16;
                                 attention with token weights: a query too large (below) */
     TQ_STATUS_BAD_LEN = 8,   /* seq_len < 0 or > max_blocks * 16 (treated as 0) */
@@ -304,8 +305,8 @@ TQ_API size_t tq_decode_weights_workspace_bytes(int B, int H_q, int head_dim, in
  *   token_weights[b][kv][t] += sum over those chunk tokens i, h of kv head kv, of
  *                              softmax_t(scale * <q[q_start[b] + i][h], k_hat_t>).
  * A short window is the usual vote on a long prompt; the whole chunk costs its scores a
- * second time.  A row whose scores are not numbers has no vote.  Arguments and checks as
- * for tq_prefill_attention, and
+ * second time.  Of a chunk longer than max_q_len the first max_q_len tokens are its chunk
+ * here, too.  Arguments and checks as for tq_prefill_attention, and
  *   token_weights  (device) fp32 [B][H_kv][weights_stride], 4-byte aligned; a seq_len
  *                  beyond weights_stride sets TQ_STATUS_BAD_LEN and gets no weights
  *   workspace      (device) >= tq_prefill_weights_workspace_bytes(...), 16-byte aligned;
@@ -348,7 +349,8 @@ TQ_API int tq_evict_select(const float* token_weights, int64_t weights_stride, c
  *             block_tables, none of them shared between sequences
  *   token_weights (device, may be NULL: no sums to move)
  *   weights_out (device) where the sums go, apart from token_weights; with
- *             dst_block_tables only (in place they move within token_weights: NULL) */
+ *             dst_block_tables only (in place they move within token_weights: NULL).  A row
+ *             of sums, there or here, shorter than seq_lens[b] is TQ_STATUS_BAD_LEN as well */
 TQ_API int tq_cache_compact(const tq_cache_t* cache, const int32_t* block_tables, int max_blocks,
                             const int32_t* seq_lens, const int32_t* kept, const int32_t* kept_lens, int B, int budget,
                             const int32_t* dst_block_tables, int dst_max_blocks, float* token_weights,
